@@ -292,6 +292,117 @@ RFB_API int rfb_attn_bwd_image_windows(const void* q, const void* k, const void*
 RFB_API int rfb_bias_project(const float* bias, const float* x, float* out, int H, int N, int k,
                              int transpose, void* stream);
 
+/*
+ * Rotary positions on queries and keys, forward and backward (one kernel for
+ * both tensors).  Pair i of a head, of rot / 2 pairs, turns by the angle
+ * t = position freqs[i]:
+ *     y1 = amplitude (x1 cos t - x2 sin t),  y2 = amplitude (x2 cos t + x1 sin t);
+ * channels from rot on pass through.  inverse != 0 turns by -t, which is the
+ * backward: the gradients of q_out, k_out in, those of q, k out.
+ *   q, k       : [B, heads, N, d] and [B, heads_kv, N, d], channels contiguous,
+ *                other strides (batch, head, token; in elements) in q_strides,
+ *                k_strides (host arrays of 3).  heads or heads_kv may be 0, its
+ *                pointers then NULL.
+ *   q_out, k_out : contiguous [B, heads(_kv), N, d]; must not alias the inputs.
+ *   positions  : device int32, position of token n of sequence b at
+ *                [b * position_stride + n] (position_stride 0: one row for all).
+ *   freqs      : device fp64 [rot / 2], angle per position in radians.
+ *   layout     : 0 pairs channel i with i + rot / 2, 1 pairs 2 i with 2 i + 1.
+ *   dtype      : 0 bf16, 1 fp16, 2 fp32 (inputs and outputs alike; the rotation
+ *                is computed in fp32 from an fp64 angle and rounded once).
+ * rot even, 0 <= rot <= d <= 1024.  Pointers need the alignment of their
+ * elements; with 16-byte aligned pointers, strides of whole 16-byte units, d a
+ * multiple of 16 bytes and rot / 2 (layout 0) or rot (layout 1) as well, the
+ * copies are 16 bytes wide.  Sequences B <= 65535.
+ */
+RFB_API int rfb_rotary(const void* q, const void* k, void* q_out, void* k_out,
+                       const int* positions, const double* freqs, int B, int heads, int heads_kv,
+                       int N, int d, int rot, const long long* q_strides,
+                       const long long* k_strides, long long position_stride, int layout,
+                       int dtype, float amplitude, int inverse, void* stream);
+
+/*
+ * The 8-bit cache of keys, values and key factors that the next three entry
+ * points share.  Owned by the caller:
+ *   k8, v8 : [B, heads_kv, cap, d] e4m3 codes, d in {32, 64, 128};
+ *   w8     : [B, heads_kv, cap, r] e4m3 codes, r in {0, 8, ..., 64} (NULL iff 0);
+ *   k_scale, v_scale, w_scale : [B, heads_kv, cap / 32] fp32, the scale of each
+ *            block of 32 tokens: a power of two, 2^ceil(log2(amax / 448)) of the
+ *            block's values with the exponent held in [-40, 40], as these calls
+ *            write it.  A value is code * scale.
+ *   mass   : [B, heads_kv, cap] fp32, the attention weight each token gathered.
+ * cap is a multiple of 32 (the capacity in tokens); sequence lengths are device
+ * int32 arrays [B], read when the kernels run, and clamped to [0, cap].  What
+ * lies behind a sequence's length is neither read into a result nor changed.
+ *
+ * Append: rows start[b] .. start[b] + counts[b] - 1 of the cache receive the
+ * first counts[b] of the n new rows; rows that would fall at or behind cap are
+ * dropped.  A block whose new rows need a larger scale has its earlier rows
+ * requantised to it (exact but for codes that become subnormal); rows are
+ * appended in order, so what the block holds behind the new rows is free.
+ * Infinities become the largest code, NaN the NaN code; neither sets a scale.
+ * Appending the same rows again changes nothing.
+ *   k, v    : [B, heads_kv, n, d] bf16, w : [B, heads_kv, n, r] bf16 (NULL iff
+ *             r == 0); channels contiguous, other strides in `strides`, a host
+ *             array of 9 (batch, head, token of k, v, w; elements, multiples of 8).
+ *   mass    : zeroed for the new rows (NULL: none kept).
+ *   start   : device int32 [B].   counts : device int32 [B], or NULL for n each.
+ * B, heads_kv <= 65535.
+ */
+RFB_API int rfb_cache_append(const void* k, const void* v, const void* w, const long long* strides,
+                             void* k8, void* v8, void* w8, float* k_scale, float* v_scale,
+                             float* w_scale, float* mass, const int* start, const int* counts,
+                             int B, int heads_kv, int n, int cap, int d, int r, void* stream);
+
+/*
+ * Attention of Nq query tokens a sequence over the cache, with the
+ * rank-factorised bias: for query i and cached token t < lengths[b]
+ *     x_t = s q . k_t + u . w_t,   O = softmax(x) V,   LSE = log(sum_t exp(x_t)).
+ * causal != 0: the queries are the sequence's last Nq tokens, and query i sees
+ * t <= lengths[b] - Nq + i.  A query that sees nothing gets O = 0, LSE = -inf.
+ * Query head h reads key head h / (heads / heads_kv).
+ *   q : [B, heads, Nq, d], u : [B, heads, Nq, r] bf16 (NULL iff r == 0).
+ *   o : [B, heads, Nq, d] bf16;  lse : [B, heads, Nq] fp32.
+ *   mass_out : if not NULL, mass_out[t] = decay * mass[t] + the sum of the
+ *       softmax weights that token t got from all queries of its key head, for
+ *       t < lengths[b]; mass may be mass_out (in place) or NULL (zeros).
+ *   workspace : device, 16-byte aligned, at least
+ *       rfb_attn_fwd_cache_workspace_size() bytes, as for rfb_attn_bwd (with
+ *       mass_out it holds the scores, 4 bytes a query row and token of capacity).
+ * heads a multiple of heads_kv; made for steps of one to some dozens of tokens
+ * (a longer prompt is read once per 64 query rows).
+ */
+RFB_API size_t rfb_attn_fwd_cache_workspace_size(int B, int heads, int heads_kv, int Nq, int cap,
+                                                 int d, int with_mass);
+RFB_API int rfb_attn_fwd_cache(const void* q, const void* u, const void* k8, const void* v8,
+                               const void* w8, const float* k_scale, const float* v_scale,
+                               const float* w_scale, const int* lengths, const float* mass,
+                               float* mass_out, float decay, void* o, float* lse, void* workspace,
+                               size_t workspace_bytes, int B, int heads, int heads_kv, int Nq,
+                               int cap, int d, int r, float scale, int causal, void* stream);
+
+/*
+ * Eviction by accumulated attention weight.  Per sequence and head, of L
+ * tokens n = min(L, keep) stay: the last rec = min(recent, n), and of those
+ * before them the n - rec of largest mass (ties go to the lowest index; NaN
+ * ranks below every number).  They move to the front in their order, with
+ * their mass.  A block of 32 whose tokens all stay where they are keeps its
+ * codes and scale; every other block gets the scale of its own values.
+ *   *_out : the cache that receives them, of capacity cap_out >= keep: all the
+ *           same pointers as the inputs (in place), or none of them.
+ *   new_lengths : int32 [B], written: n (not the lengths array itself).
+ *   kept  : int32 [B, heads_kv, keep], written: the tokens' former positions,
+ *           -1 behind the last.
+ * 1 <= keep.  Entries behind n are left as they are.
+ */
+RFB_API int rfb_cache_evict(const void* k8, const void* v8, const void* w8, const float* k_scale,
+                            const float* v_scale, const float* w_scale, const float* mass,
+                            void* k8_out, void* v8_out, void* w8_out, float* k_scale_out,
+                            float* v_scale_out, float* w_scale_out, float* mass_out,
+                            const int* lengths, int* new_lengths, int* kept, int B, int heads_kv,
+                            int cap, int cap_out, int d, int r, int keep, int recent,
+                            void* stream);
+
 /* Human-readable text for a status code (static storage). */
 RFB_API const char* rfb_strerror(int status);
 

@@ -41,6 +41,11 @@ SIGNATURES = {
     "rfb_attn_bwd_image_windows": (_i, [_vp] * 6 + [_fp] + [_vp] * 7 + [_sz] + [_i] * 8
                                    + [_f, _vp]),
     "rfb_attn_bwd_shared_bias": (_i, [_vp] * 6 + [_fp] + [_vp] * 7 + [_sz] + [_i] * 5 + [_f, _vp]),
+    "rfb_rotary": (_i, [_vp] * 6 + [_i] * 6 + [_vp] * 2 + [ctypes.c_longlong, _i, _i, _f, _i, _vp]),
+    "rfb_cache_append": (_i, [_vp] * 13 + [_i] * 6 + [_vp]),
+    "rfb_attn_fwd_cache_workspace_size": (_sz, [_i] * 7),
+    "rfb_attn_fwd_cache": (_i, [_vp] * 11 + [_f] + [_vp] * 3 + [_sz] + [_i] * 7 + [_f, _i, _vp]),
+    "rfb_cache_evict": (_i, [_vp] * 17 + [_i] * 8 + [_vp]),
     "rfb_strerror": (ctypes.c_char_p, [_i]),
     "rfb_last_device_error": (_i, []),
     "rfb_last_cuda_error": (_i, [ctypes.POINTER(ctypes.c_int)]),

@@ -32,7 +32,8 @@ def _nvcc() -> str:
 
 
 def sources():
-    return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh"))
+    return sorted(glob.glob(os.path.join(CSRC, "**", "*.cu"), recursive=True)
+                  + glob.glob(os.path.join(CSRC, "**", "*.cuh"), recursive=True)
                   + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
@@ -50,7 +51,7 @@ def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = True) 
     cmd = [_nvcc(), *ARCH, "-O3", "-std=c++17", "-lineinfo", "-shared",
            "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
            "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC,
-           "-o", tmp, os.path.join(CSRC, "rfb_attn.cu")]
+           "-o", tmp, os.path.join(CSRC, "serve", "rfb_library.cu")]
     if ptxas_verbose:
         cmd += ["-Xptxas", "-v"]
     res = subprocess.run(cmd, capture_output=True, text=True)

@@ -1,0 +1,113 @@
+// cache_append.cuh -- new rows of K, V (and the bias factor W) into the 8-bit
+// cache.
+//
+// One warp owns one block of 32 tokens of one head and tensor, so a block's
+// scale and codes have one writer and nothing is atomic: it takes the largest
+// magnitude of the block's new rows, grows the scale if the rows before them
+// have a smaller one (requantising those rows), and writes the new codes.
+// Reads 2 bytes and writes 1 per element: bound by HBM for prompts, by latency
+// for single tokens.
+#pragma once
+#include "../sm100.cuh"
+#include "e4m3.cuh"
+
+namespace rfb {
+
+constexpr int kAppendWarps = 4;
+
+struct AppendArgs {
+  const __nv_bfloat16* x[3];      // new k, v, w
+  long long sb[3], sh[3], sn[3];  // strides in elements (rows of contiguous channels)
+  uint8_t* codes[3];              // [B, Hk, cap, c]
+  float* scales[3];               // [B, Hk, cap / 32]
+  float* mass;                    // [B, Hk, cap] or null: zeroed for the new tokens
+  const int* start;               // [B]
+  const int* counts;              // [B] or null (all n)
+  int Hk, n, cap, d, r, blocks, tensors;
+};
+
+// CPR: 8-channel chunks of a row (0: r / 8, at most 8).
+template <int CPR>
+__device__ __forceinline__ void append_block(const AppendArgs& a, int z, int b, int h, int lo,
+                                             int start, int end) {
+  constexpr int ITS = CPR ? CPR : 8;
+  const int cpr = CPR ? CPR : a.r / 8;
+  const int lane = lane_id();
+  const __nv_bfloat16* x = a.x[z] + b * a.sb[z] + h * a.sh[z];
+  uint4 v[ITS];
+  uint32_t top = 0;
+#pragma unroll
+  for (int it = 0; it < ITS; ++it) {
+    const int i = it * 32 + lane, row = i / cpr, t = lo + row;
+    v[it] = make_uint4(0, 0, 0, 0);
+    if (it < cpr && t >= start && t < end)
+      v[it] = __ldg(reinterpret_cast<const uint4*>(x + (t - start) * a.sn[z] + (i - row * cpr) * 8));
+  }
+#pragma unroll
+  for (int it = 0; it < ITS; ++it) {
+    const uint32_t w[4] = {v[it].x, v[it].y, v[it].z, v[it].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t m = w[k] & 0x7fff7fffu;  // magnitudes; infinities and NaN do not set a scale
+      top = __vmaxu2(top, m & ~__vcmpgeu2(m, 0x7f807f80u));
+    }
+  }
+  top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+  const long long bh = static_cast<long long>(b) * a.Hk + h;
+  float* sp = a.scales[z] + bh * (a.cap / kCacheBlock) + lo / kCacheBlock;
+  uint8_t* codes = a.codes[z] + (bh * a.cap + lo) * (cpr * 8);
+  float s = scale_for(__uint_as_float(top << 16));
+  const int before = start - lo;  // rows of the block that are there already
+  if (before > 0) {
+    const float was = *sp;
+    s = fmaxf(s, was);
+    if (s != was) {
+      const float ratio = was / s;
+      for (int i = lane; i < before * cpr; i += 32) {
+        uint2* p = reinterpret_cast<uint2*>(codes) + i;
+        const uint2 c = *p;
+        *p = make_uint2(requantise4(c.x, ratio), requantise4(c.y, ratio));
+      }
+    }
+  }
+  const float inv = 1.0f / s;
+#pragma unroll
+  for (int it = 0; it < ITS; ++it) {
+    const int i = it * 32 + lane, row = i / cpr, t = lo + row;
+    if (it < cpr && t >= start && t < end) {
+      const uint32_t w[4] = {v[it].x, v[it].y, v[it].z, v[it].w};
+      uint32_t o[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        o[k] = f32x2_to_e4m3x2(__uint_as_float(w[k] << 16) * inv,
+                               __uint_as_float(w[k] & 0xffff0000u) * inv);
+      reinterpret_cast<uint2*>(codes)[i] = make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+    }
+  }
+  __syncwarp();  // every lane has read the old scale
+  if (lane == 0) *sp = s;
+  if (z == 0 && a.mass != nullptr) {
+    const int t = lo + lane;
+    if (t >= start && t < end) a.mass[bh * a.cap + t] = 0.0f;
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kAppendWarps * 32) cache_append_kernel(const AppendArgs a) {
+  grid_dep_wait();
+  const int unit = blockIdx.x * kAppendWarps + warp_id();
+  const int j = unit / a.tensors, z = unit - j * a.tensors;
+  if (j >= a.blocks) return;
+  const int b = blockIdx.z, h = blockIdx.y;
+  const int start = min(max(a.start[b], 0), a.cap);
+  const int n = a.counts ? min(max(a.counts[b], 0), a.n) : a.n;
+  const int end = start + min(n, a.cap - start);  // rows beyond the capacity are dropped
+  const long long lo = (static_cast<long long>(start / kCacheBlock) + j) * kCacheBlock;
+  if (lo >= end || end == start) return;
+  if (z == 2)
+    append_block<0>(a, z, b, h, static_cast<int>(lo), start, end);
+  else
+    append_block<D / 8>(a, z, b, h, static_cast<int>(lo), start, end);
+}
+
+}  // namespace rfb

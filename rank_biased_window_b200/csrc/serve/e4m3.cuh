@@ -1,0 +1,58 @@
+// e4m3.cuh -- the 8-bit format of the key / value cache: e4m3 codes with one
+// scale per head and 32 tokens.
+//
+// A scale is a power of two, 2^ceil(log2(amax / 448)) with the exponent held
+// in [-40, 40] (448 is the largest e4m3 value), so multiplying by it is exact:
+// a value's code does not depend on how the division is rounded, and moving a
+// code to a larger scale rounds only codes that become subnormal.
+#pragma once
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+namespace rfb {
+
+constexpr int kCacheBlock = 32;  // tokens per scale
+constexpr int kScaleMinExp = -40, kScaleMaxExp = 40;
+
+__device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }
+
+// Scale for values of largest magnitude amax (finite, >= 0), from the bits of
+// amax as fp32: amax = m 2^e with m in [1/2, 1); 448 = 0.875 2^9.
+__device__ __forceinline__ float scale_for(float amax) {
+  const int bits = __float_as_int(amax);
+  int e = (bits >> 23) - 126;                       // subnormal and zero amax: far below the floor
+  e = (bits & 0x7fffff) > 0x600000 ? e - 8 : e - 9;  // m > 0.875
+  return pow2f(min(max(e, kScaleMinExp), kScaleMaxExp));
+}
+
+// Two e4m3 codes (the low 16 bits of a register) as two fp16 values; exact.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t v) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(v));
+  return r;
+}
+__device__ __forceinline__ float2 e4m3x2_to_f32x2(uint16_t v) {
+  const uint32_t h = e4m3x2_to_f16x2(v);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+// Round to nearest even; magnitudes above 448 become 448, NaN the NaN code.
+__device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Four codes to a scale that is 1 / ratio times theirs.
+__device__ __forceinline__ uint32_t requantise4(uint32_t v, float ratio) {
+  const float2 a = e4m3x2_to_f32x2(static_cast<uint16_t>(v));
+  const float2 b = e4m3x2_to_f32x2(static_cast<uint16_t>(v >> 16));
+  return f32x2_to_e4m3x2(a.x * ratio, a.y * ratio) |
+         (f32x2_to_e4m3x2(b.x * ratio, b.y * ratio) << 16);
+}
+// Magnitude codes of four bytes, the NaN code (0x7f) counted as 0.
+__device__ __forceinline__ uint32_t finite_mag4(uint32_t v) {
+  const uint32_t m = v & 0x7f7f7f7fu;
+  return m & ~__vcmpeq4(m, 0x7f7f7f7fu);
+}
+
+}  // namespace rfb

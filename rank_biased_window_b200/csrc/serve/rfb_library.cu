@@ -1,0 +1,340 @@
+// rfb_library.cu -- the library's one translation unit: the attention entry
+// points of rfb_attn.cu, and the host side of the serving operators (rotary
+// positions, 8-bit cache append, attention over the cache, eviction), which
+// share its error record, device queries and launch helpers.
+#include "../rfb_attn.cu"
+
+#include "cache_append.cuh"
+#include "cache_attn.cuh"
+#include "cache_evict.cuh"
+#include "rotary.cuh"
+
+namespace rfb {
+namespace {
+
+bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// ------------------------------------------------------------------ rotary
+template <typename T, bool HALF, bool VEC>
+int launch_rotary(RotArgs& a, int B, int sms, cudaStream_t st) {
+  const int pairs = !VEC ? 1 : HALF ? Rot<T>::VEC : Rot<T>::VEC / 2;
+  a.units = a.rot / (2 * pairs) + (a.d - a.rot) / (VEC ? Rot<T>::VEC : 1);
+  // One thread per unit and group of heads.  More heads a thread share the
+  // sine and cosine; fewer fill the chip: halve the group until there are 512
+  // threads an SM (below that the call is latency, and one head is shortest).
+  const int heads = a.heads[0] + a.heads[1];
+  const double units = static_cast<double>(B) * a.N * a.units;
+  int per = heads;
+  while (per > 1 && units * ((heads + per - 1) / per) < 512.0 * sms) per = (per + 1) / 2;
+  a.heads_per_thread = per;
+  const long long blocks =
+      (static_cast<long long>(a.N) * a.units + kRotThreads - 1) / kRotThreads;
+  const int groups = (heads + per - 1) / per;
+  if (blocks > 0x7fffffffLL || B > 65535 || groups > 65535) return RFB_ERR_UNSUPPORTED;
+  const dim3 grid(static_cast<unsigned>(blocks), groups, B);
+  launch_pdl(rotary_kernel<T, HALF, VEC>, grid, dim3(kRotThreads), 0, st, a);
+  return launch_status();
+}
+
+template <typename T>
+int dispatch_rotary(RotArgs& a, int B, bool half, int sms, cudaStream_t st) {
+  constexpr int V = Rot<T>::VEC;
+  bool vec = a.d % V == 0 && a.rot % (half ? 2 * V : V) == 0;
+  for (int z = 0; z < 2; ++z)
+    vec = vec && (a.heads[z] == 0 || (aligned16(a.x[z]) && aligned16(a.y[z]) &&
+                                      a.sb[z] % V == 0 && a.sh[z] % V == 0 && a.sn[z] % V == 0));
+  if (half)
+    return vec ? launch_rotary<T, true, true>(a, B, sms, st)
+               : launch_rotary<T, true, false>(a, B, sms, st);
+  return vec ? launch_rotary<T, false, true>(a, B, sms, st)
+             : launch_rotary<T, false, false>(a, B, sms, st);
+}
+
+// ------------------------------------------------------------------- cache
+// Sizes shared by the cache entry points.  RFB_OK with *empty set when there
+// is no head, row or token to work on.
+int check_cache(int B, int heads_kv, int cap, int d, int r) {
+  if (B < 0 || heads_kv < 0 || cap < 0 || d < 0 || r < 0) return RFB_ERR_INVALID_ARG;
+  if (d != 32 && d != 64 && d != 128) return RFB_ERR_UNSUPPORTED;
+  if (r > 64 || r % 8 != 0 || cap % kCacheBlock != 0) return RFB_ERR_UNSUPPORTED;
+  if (static_cast<long long>(B) * heads_kv > 0x7fffffffLL / 4) return RFB_ERR_UNSUPPORTED;
+  return RFB_OK;
+}
+
+// Row tiles and CTAs of the attention over the cache.
+struct CaPlan {
+  int wr, row_segs, seg_rows, ctas;
+  size_t ml_bytes, o_bytes, score_bytes;
+};
+
+size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
+CaPlan plan_cache_attn(int B, int Hk, int R, int cap, int d, bool mass, int sms) {
+  CaPlan p;
+  const int tiles = (R + 15) / 16;
+  p.wr = tiles >= 3 ? 4 : tiles;
+  p.row_segs = (tiles + p.wr - 1) / p.wr;
+  p.seg_rows = R < 16 * p.wr ? R : 16 * p.wr;
+  // One wave of resident CTAs, fewer when that would leave warps without a block.
+  const long long blocks = static_cast<long long>(B) * Hk * p.row_segs * (cap / kCacheBlock);
+  const int wts = kCaWarps / p.wr;
+  const long long most = (blocks + wts - 1) / wts;
+  const int wave = sms * (d == 128 ? 2 : 3);
+  p.ctas = static_cast<int>(most < wave ? (most > 0 ? most : 1) : wave);
+  p.ml_bytes = round256(static_cast<size_t>(p.ctas) * 2 * p.seg_rows * sizeof(float2));
+  p.o_bytes = round256(static_cast<size_t>(p.ctas) * 2 * p.seg_rows * d * sizeof(float));
+  p.score_bytes = mass ? static_cast<size_t>(B) * Hk * R * cap * sizeof(float) : 0;
+  return p;
+}
+
+template <int D, int RP>
+int launch_cache_attn(const CacheAttnArgs& a, int ctas, cudaStream_t st) {
+  if (a.scores)
+    launch_pdl(cache_attn_kernel<D, RP, true>, dim3(ctas), dim3(kCaThreads), 0, st, a);
+  else
+    launch_pdl(cache_attn_kernel<D, RP, false>, dim3(ctas), dim3(kCaThreads), 0, st, a);
+  if (int rc = launch_status()) return rc;
+  const int rows_per = 128 / (D / 4), seg_rows = a.R < 16 * a.wr ? a.R : 16 * a.wr;
+  const dim3 grid(static_cast<unsigned>(a.B * a.Hk * a.row_segs),
+                  (seg_rows + rows_per - 1) / rows_per);
+  launch_pdl(cache_attn_combine_kernel<D>, grid, dim3(128), 0, st, a, ctas);
+  return launch_status();
+}
+
+template <int D>
+int dispatch_cache_attn(const CacheAttnArgs& a, int ctas, cudaStream_t st) {
+  switch (pad_rank(a.r)) {
+    case 0: return launch_cache_attn<D, 0>(a, ctas, st);
+    case 16: return launch_cache_attn<D, 16>(a, ctas, st);
+    case 32: return launch_cache_attn<D, 32>(a, ctas, st);
+    default: return launch_cache_attn<D, 64>(a, ctas, st);
+  }
+}
+
+}  // namespace
+}  // namespace rfb
+
+using namespace rfb;
+
+extern "C" {
+
+int rfb_rotary(const void* q, const void* k, void* q_out, void* k_out, const int* positions,
+               const double* freqs, int B, int heads, int heads_kv, int N, int d, int rot,
+               const long long* q_strides, const long long* k_strides, long long position_stride,
+               int layout, int dtype, float amplitude, int inverse, void* stream) {
+  if (B < 0 || heads < 0 || heads_kv < 0 || N < 0 || d < 0 || rot < 0) return RFB_ERR_INVALID_ARG;
+  if ((layout != 0 && layout != 1) || dtype < 0 || dtype > 2 || !std::isfinite(amplitude) ||
+      position_stride < 0)
+    return RFB_ERR_INVALID_ARG;
+  if (rot % 2 != 0 || rot > d || d > 1024 || heads > 65535 || heads_kv > 65535)
+    return RFB_ERR_UNSUPPORTED;
+  if (B == 0 || N == 0 || d == 0 || heads + heads_kv == 0) return RFB_OK;
+  if ((heads > 0 && (!q || !q_out || !q_strides)) ||
+      (heads_kv > 0 && (!k || !k_out || !k_strides)) || !positions || (rot > 0 && !freqs))
+    return RFB_ERR_INVALID_ARG;
+  const size_t elem = dtype == 2 ? 4 : 2;
+  if (!aligned_to(q, elem) || !aligned_to(k, elem) || !aligned_to(q_out, elem) ||
+      !aligned_to(k_out, elem) || !aligned_to(positions, 4) || !aligned_to(freqs, 8))
+    return RFB_ERR_ALIGNMENT;
+  DeviceInfo dev;
+  if (int rc = device_info(&dev)) return rc;
+  RotArgs a = {};
+  a.x[0] = q, a.x[1] = k;
+  a.y[0] = q_out, a.y[1] = k_out;
+  a.heads[0] = heads, a.heads[1] = heads_kv;
+  for (int z = 0; z < 2; ++z) {
+    const long long* s = z ? k_strides : q_strides;
+    if (a.heads[z] == 0) continue;
+    a.sb[z] = s[0], a.sh[z] = s[1], a.sn[z] = s[2];
+  }
+  a.pos = positions;
+  a.freq = freqs;
+  a.pos_sb = position_stride;
+  a.N = N, a.d = d, a.rot = rot;
+  a.amp = amplitude;
+  a.sign = inverse ? -1.f : 1.f;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool half = layout == 0;
+  if (dtype == 0) return dispatch_rotary<__nv_bfloat16>(a, B, half, dev.sms, st);
+  if (dtype == 1) return dispatch_rotary<__half>(a, B, half, dev.sms, st);
+  return dispatch_rotary<float>(a, B, half, dev.sms, st);
+}
+
+int rfb_cache_append(const void* k, const void* v, const void* w, const long long* strides,
+                     void* k8, void* v8, void* w8, float* k_scale, float* v_scale, float* w_scale,
+                     float* mass, const int* start, const int* counts, int B, int heads_kv, int n,
+                     int cap, int d, int r, void* stream) {
+  if (n < 0) return RFB_ERR_INVALID_ARG;
+  if (int rc = check_cache(B, heads_kv, cap, d, r)) return rc;
+  if (B > 65535 || heads_kv > 65535) return RFB_ERR_UNSUPPORTED;
+  if (B == 0 || heads_kv == 0 || n == 0 || cap == 0) return RFB_OK;
+  if (!k || !v || !k8 || !v8 || !k_scale || !v_scale || !start || !strides ||
+      (r > 0 && (!w || !w8 || !w_scale)))
+    return RFB_ERR_INVALID_ARG;
+  AppendArgs a = {};
+  const void* x[3] = {k, v, w};
+  void* c[3] = {k8, v8, w8};
+  float* s[3] = {k_scale, v_scale, w_scale};
+  a.tensors = r > 0 ? 3 : 2;
+  for (int z = 0; z < a.tensors; ++z) {
+    if (!aligned16(x[z]) || !aligned16(c[z]) || !aligned16(s[z])) return RFB_ERR_ALIGNMENT;
+    a.x[z] = static_cast<const __nv_bfloat16*>(x[z]);
+    a.codes[z] = static_cast<uint8_t*>(c[z]);
+    a.scales[z] = s[z];
+    a.sb[z] = strides[3 * z], a.sh[z] = strides[3 * z + 1], a.sn[z] = strides[3 * z + 2];
+    if (a.sb[z] % 8 || a.sh[z] % 8 || a.sn[z] % 8) return RFB_ERR_ALIGNMENT;
+  }
+  if (!aligned16(mass) || !aligned_to(start, 4) || !aligned_to(counts, 4)) return RFB_ERR_ALIGNMENT;
+  a.mass = mass;
+  a.start = start;
+  a.counts = counts;
+  a.Hk = heads_kv, a.n = n, a.cap = cap, a.d = d, a.r = r;
+  a.blocks = static_cast<int>((static_cast<long long>(n) + kCacheBlock - 2) / kCacheBlock) + 1;
+  if (a.blocks > cap / kCacheBlock) a.blocks = cap / kCacheBlock;
+  DeviceInfo dev;
+  if (int rc = device_info(&dev)) return rc;
+  const long long units = static_cast<long long>(a.blocks) * a.tensors;
+  const dim3 grid(static_cast<unsigned>((units + kAppendWarps - 1) / kAppendWarps), heads_kv, B);
+  const dim3 block(kAppendWarps * 32);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (d == 32) launch_pdl(cache_append_kernel<32>, grid, block, 0, st, a);
+  else if (d == 64) launch_pdl(cache_append_kernel<64>, grid, block, 0, st, a);
+  else launch_pdl(cache_append_kernel<128>, grid, block, 0, st, a);
+  return launch_status();
+}
+
+size_t rfb_attn_fwd_cache_workspace_size(int B, int heads, int heads_kv, int Nq, int cap, int d,
+                                         int with_mass) {
+  if (check_cache(B, heads_kv, cap, d, 0) || heads_kv == 0 || heads < 0 || Nq < 0 ||
+      heads % heads_kv != 0)
+    return 0;
+  const long long R = static_cast<long long>(heads / heads_kv) * Nq;
+  if (B == 0 || R == 0 || R > 0x7fffffffLL) return 0;
+  DeviceInfo dev;
+  if (device_info(&dev)) return 0;
+  const CaPlan p = plan_cache_attn(B, heads_kv, static_cast<int>(R), cap, d, with_mass != 0, dev.sms);
+  return p.ml_bytes + p.o_bytes + p.score_bytes;
+}
+
+int rfb_attn_fwd_cache(const void* q, const void* u, const void* k8, const void* v8, const void* w8,
+                       const float* k_scale, const float* v_scale, const float* w_scale,
+                       const int* lengths, const float* mass, float* mass_out, float decay, void* o,
+                       float* lse, void* workspace, size_t workspace_bytes, int B, int heads,
+                       int heads_kv, int Nq, int cap, int d, int r, float scale, int causal,
+                       void* stream) {
+  if (heads < 0 || Nq < 0 || !std::isfinite(scale) || !(scale > 0.f) || !std::isfinite(decay))
+    return RFB_ERR_INVALID_ARG;
+  if (int rc = check_cache(B, heads_kv, cap, d, r)) return rc;
+  if (B == 0 || heads == 0 || Nq == 0) return RFB_OK;
+  if (heads_kv == 0 || heads % heads_kv != 0) return RFB_ERR_INVALID_ARG;
+  const long long R = static_cast<long long>(heads / heads_kv) * Nq;
+  if (R > (1LL << 24) || static_cast<long long>(B) * heads_kv * ((R + 15) / 16) > 0x7fffffffLL ||
+      (mass_out && cap > 65535 * 512))
+    return RFB_ERR_UNSUPPORTED;
+  if (!q || !o || !lse || !lengths || (r > 0 && !u) ||
+      (cap > 0 && (!k8 || !v8 || !k_scale || !v_scale || (r > 0 && (!w8 || !w_scale)))))
+    return RFB_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(u) || !aligned16(k8) || !aligned16(v8) || !aligned16(w8) ||
+      !aligned16(o) || !aligned16(lse) || !aligned16(k_scale) || !aligned16(v_scale) ||
+      !aligned16(w_scale) || !aligned16(mass) || !aligned16(mass_out) || !aligned_to(lengths, 4))
+    return RFB_ERR_ALIGNMENT;
+  DeviceInfo dev;
+  if (int rc = device_info(&dev)) return rc;
+  const CaPlan p = plan_cache_attn(B, heads_kv, static_cast<int>(R), cap, d, mass_out != nullptr,
+                                   dev.sms);
+  if (!workspace || workspace_bytes < p.ml_bytes + p.o_bytes + p.score_bytes)
+    return RFB_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return RFB_ERR_ALIGNMENT;
+  CacheAttnArgs a = {};
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.u = static_cast<const __nv_bfloat16*>(u);
+  a.k = static_cast<const uint8_t*>(k8);
+  a.v = static_cast<const uint8_t*>(v8);
+  a.w = static_cast<const uint8_t*>(w8);
+  a.ks = k_scale, a.vs = v_scale, a.ws = w_scale;
+  a.lengths = lengths;
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.lse = lse;
+  char* ws = static_cast<char*>(workspace);
+  a.part_ml = reinterpret_cast<float2*>(ws);
+  a.part_o = reinterpret_cast<float*>(ws + p.ml_bytes);
+  a.scores = mass_out ? reinterpret_cast<float*>(ws + p.ml_bytes + p.o_bytes) : nullptr;
+  a.B = B, a.Hk = heads_kv, a.R = static_cast<int>(R), a.Nq = Nq, a.cap = cap, a.r = r;
+  a.wr = p.wr, a.row_segs = p.row_segs;
+  a.causal = causal;
+  a.scale_log2 = scale * kLog2e;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int rc = d == 32   ? dispatch_cache_attn<32>(a, p.ctas, st)
+           : d == 64 ? dispatch_cache_attn<64>(a, p.ctas, st)
+                     : dispatch_cache_attn<128>(a, p.ctas, st);
+  if (rc != RFB_OK || !mass_out || cap == 0) return rc;
+  const dim3 grid(static_cast<unsigned>(B) * heads_kv, (cap + 511) / 512);
+  launch_pdl(cache_mass_kernel, grid, dim3(128), 0, st, a, mass, mass_out, decay);
+  return launch_status();
+}
+
+int rfb_cache_evict(const void* k8, const void* v8, const void* w8, const float* k_scale,
+                    const float* v_scale, const float* w_scale, const float* mass, void* k8_out,
+                    void* v8_out, void* w8_out, float* k_scale_out, float* v_scale_out,
+                    float* w_scale_out, float* mass_out, const int* lengths, int* new_lengths,
+                    int* kept, int B, int heads_kv, int cap, int cap_out, int d, int r, int keep,
+                    int recent, void* stream) {
+  if (keep < 1 || recent < 0 || cap_out < 0) return RFB_ERR_INVALID_ARG;
+  if (int rc = check_cache(B, heads_kv, cap, d, r)) return rc;
+  if (cap_out % kCacheBlock != 0) return RFB_ERR_UNSUPPORTED;
+  if (keep > cap_out) return RFB_ERR_INVALID_ARG;
+  if (B == 0 || heads_kv == 0) return RFB_OK;
+  const void* c[3] = {k8, v8, w8};
+  void* co[3] = {k8_out, v8_out, w8_out};
+  const float* s[3] = {k_scale, v_scale, w_scale};
+  float* so[3] = {k_scale_out, v_scale_out, w_scale_out};
+  EvictArgs a = {};
+  a.tensors = r > 0 ? 3 : 2;
+  int same = 0;
+  for (int z = 0; z < a.tensors; ++z) {
+    if (!c[z] || !co[z] || !s[z] || !so[z]) return RFB_ERR_INVALID_ARG;
+    if (!aligned16(c[z]) || !aligned16(co[z]) || !aligned16(s[z]) || !aligned16(so[z]))
+      return RFB_ERR_ALIGNMENT;
+    same += (c[z] == co[z]) + (s[z] == so[z]);
+    a.codes[z] = static_cast<const uint8_t*>(c[z]);
+    a.to_codes[z] = static_cast<uint8_t*>(co[z]);
+    a.scales[z] = s[z];
+    a.to_scales[z] = so[z];
+  }
+  if (!mass || !mass_out || !lengths || !new_lengths || !kept || lengths == new_lengths)
+    return RFB_ERR_INVALID_ARG;
+  if (!aligned16(mass) || !aligned16(mass_out) || !aligned_to(lengths, 4) ||
+      !aligned_to(new_lengths, 4) || !aligned_to(kept, 4))
+    return RFB_ERR_ALIGNMENT;
+  same += mass == mass_out;
+  const int all = 2 * a.tensors + 1;
+  if (same != 0 && (same != all || cap != cap_out)) return RFB_ERR_INVALID_ARG;  // all or none
+  a.in_place = same == all;
+  a.mass = mass;
+  a.to_mass = mass_out;
+  a.lengths = lengths;
+  a.new_lengths = new_lengths;
+  a.kept = kept;
+  a.Hk = heads_kv, a.cap = cap, a.to_cap = cap_out, a.d = d, a.r = r;
+  a.keep = keep, a.recent = recent;
+  DeviceInfo dev;
+  if (int rc = device_info(&dev)) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int bh = B * heads_kv;
+  launch_pdl(cache_select_kernel, dim3(bh), dim3(kSelThreads), 0, st, a);
+  if (int rc = launch_status()) return rc;
+  // Out of place, enough parts for two CTAs an SM; in place the blocks go in order.
+  int parts = 1;
+  if (!a.in_place) {
+    const int most = (keep + kCacheBlock * kMoveWarps - 1) / (kCacheBlock * kMoveWarps);
+    const int want = (2 * dev.sms + bh * a.tensors - 1) / (bh * a.tensors);
+    parts = want < most ? want : most;
+  }
+  const dim3 grid(static_cast<unsigned>(bh) * (a.tensors + 1), parts), block(kMoveWarps * 32);
+  if (d == 32) launch_pdl(cache_move_kernel<32>, grid, block, 0, st, a);
+  else if (d == 64) launch_pdl(cache_move_kernel<64>, grid, block, 0, st, a);
+  else launch_pdl(cache_move_kernel<128>, grid, block, 0, st, a);
+  return launch_status();
+}
+
+}  // extern "C"
