@@ -45,48 +45,94 @@ struct CacheAttnArgs {
   float* part_o;  // [ctas][2][rows of a segment][d]
   float2* part_ml;
   int B, Hk, R, Nq, cap, r;
+  int tile;      // queries of a warp: 8 or 16
   int wr;        // warps over row tiles: 1, 2 or 4
-  int row_segs;  // segments of 16 wr rows
+  int row_segs;  // segments of tile * wr rows
   int causal;
+  int stages;
   float scale_log2;
+  int* err_word;
+  unsigned long long wait_ns;
+  int fail_site;
 };
 
 __device__ __forceinline__ int cache_blocks(const CacheAttnArgs& a, int b) {
   return (min(max(a.lengths[b], 0), a.cap) + kCacheBlock - 1) / kCacheBlock;
 }
 
-// Blocks of sequences [0, b_end) (all lanes of the warp call it).
-__device__ __forceinline__ long long blocks_before(const CacheAttnArgs& a, int b_end) {
-  long long sum = 0;
-  for (int b0 = 0; b0 < b_end; b0 += 32) {
-    const int b = b0 + static_cast<int>(lane_id());
-    const unsigned n = b < b_end ? cache_blocks(a, b) : 0;
-    sum += __reduce_add_sync(0xffffffffu, n);
+// Blocks of all sequences, and of those before sequence b (all lanes call it).
+__device__ __forceinline__ void count_blocks(const CacheAttnArgs& a, int b, unsigned& before,
+                                             unsigned& total) {
+  before = total = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const int x = b0 + static_cast<int>(lane_id());
+    const unsigned n = x < a.B ? cache_blocks(a, x) : 0;
+    total += __reduce_add_sync(0xffffffffu, n);
+    before += __reduce_add_sync(0xffffffffu, x < b ? n : 0u);
   }
-  return sum;
 }
 
-// Sequence that holds block `at` of the per-sequence line, and the blocks before it.
-__device__ __forceinline__ int sequence_of(const CacheAttnArgs& a, long long at, long long& before) {
-  before = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const int b = b0 + static_cast<int>(lane_id());
-    const int n = b < a.B ? cache_blocks(a, b) : 0;
-    int incl = n;
+// The line of W blocks cut over n CTAs: the first W % n hold W / n + 1, the rest W / n.
+struct Cut {
+  unsigned base, extra;
+  __device__ __forceinline__ Cut(unsigned W, unsigned n) : base(W / n), extra(W - W / n * n) {}
+  __device__ __forceinline__ unsigned start(unsigned i) const { return i * base + min(i, extra); }
+  __device__ __forceinline__ unsigned holder(unsigned x) const {
+    const unsigned fat = extra * (base + 1);
+    return x < fat ? x / (base + 1) : extra + (x - fat) / max(base, 1u);
+  }
+};
+
+// The CTA's part [at, stop) of the line and where it starts: sequence b, whose
+// segments have nb blocks each; segment seg of it, block blk.
+struct Place {
+  unsigned at, stop;
+  int b, nb, seg, blk;
+};
+__device__ __forceinline__ Place place_of(const CacheAttnArgs& a, unsigned mult) {
+  Place p = {};
+  const int lane = lane_id();
+  unsigned total = 0, n = 0, incl = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {  // at most 32 sequences: one round, kept below
+    n = b0 + lane < a.B ? cache_blocks(a, b0 + lane) : 0;
+    incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, incl, o);
-      if (static_cast<int>(lane_id()) >= o) incl += x;
+      const unsigned x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
     }
-    const unsigned past = __ballot_sync(0xffffffffu, before + incl > at);
+    total += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  const Cut cut(total * mult, gridDim.x);
+  p.at = cut.start(blockIdx.x);
+  p.stop = cut.start(blockIdx.x + 1);
+  if (p.at >= p.stop) return p;
+  const unsigned seq_at = p.at / mult;
+  unsigned before = 0;
+  for (int b0 = 0;; b0 += 32) {
+    if (a.B > 32) {
+      n = b0 + lane < a.B ? cache_blocks(a, b0 + lane) : 0;
+      incl = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+      }
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, before + incl > seq_at);
     if (past) {
       const int l = __ffs(past) - 1;
       before += __shfl_sync(0xffffffffu, incl - n, l);
-      return b0 + l;
+      p.b = b0 + l;
+      p.nb = __shfl_sync(0xffffffffu, n, l);
+      break;
     }
     before += __shfl_sync(0xffffffffu, incl, 31);
   }
-  return a.B;
+  const unsigned in_seq = p.at - before * mult;
+  p.seg = in_seq / p.nb;
+  p.blk = in_seq - p.seg * p.nb;
+  return p;
 }
 
 __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -100,32 +146,36 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ uint32_t e4m3_lo(uint32_t w) {
-  return e4m3x2_to_f16x2(static_cast<uint16_t>(w));
-}
-__device__ __forceinline__ uint32_t e4m3_hi(uint32_t w) {
-  return e4m3x2_to_f16x2(static_cast<uint16_t>(w >> 16));
+// An 8 x 8 tile of 16-bit values, a row in the lanes of one g, transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
 
-// O += P V for 16 rows and 32 tokens: p[kk] the A fragments of tokens 16 kk..,
-// v[4 kk + i] the lane's piece of its i-th token there.  Channel tile n of the
-// product holds channel g (D / 8) + n in column g.
-template <int VW>
-__device__ __forceinline__ void pv_product(const uint32_t (*p)[4], const uint32_t (*v)[VW],
-                                           float (*o)[4]) {
+// O^T += V^T P^T for 16 tokens and 8 QT queries: v[i] the lane's piece of its i-th
+// token (two of columns 2 t, 2 t + 1, two of the next 8), word w of it, i.e. channels
+// g (D / 8) + 4 w + {0..3}, which are rows g and g + 8 of channel tiles 2 w, 2 w + 1.
+template <int VW, int QT>
+__device__ __forceinline__ void pv_words(const uint32_t (*p)[2], const uint32_t (*v)[VW], int w,
+                                         float (*o)[QT][4]) {
+  const uint32_t a01 = __byte_perm(v[0][w], v[1][w], 0x5140);
+  const uint32_t a23 = __byte_perm(v[0][w], v[1][w], 0x7362);
+  const uint32_t b01 = __byte_perm(v[2][w], v[3][w], 0x5140);
+  const uint32_t b23 = __byte_perm(v[2][w], v[3][w], 0x7362);
+  const uint32_t lo[4] = {e4m3_lo(a01), e4m3_hi(a01), e4m3_lo(b01), e4m3_hi(b01)};
+  const uint32_t hi[4] = {e4m3_lo(a23), e4m3_hi(a23), e4m3_lo(b23), e4m3_hi(b23)};
 #pragma unroll
-  for (int kk = 0; kk < 2; ++kk)
+  for (int q = 0; q < QT; ++q) {
+    mma_f16(o[0][q], lo, p[q][0], p[q][1]);
+    mma_f16(o[1][q], hi, p[q][0], p[q][1]);
+  }
+}
+template <int VW, int QT>
+__device__ __forceinline__ void pv_step(const uint32_t (*p)[2], const uint32_t (*v)[VW],
+                                        float (*o)[QT][4]) {
 #pragma unroll
-    for (int w = 0; w < VW; ++w) {
-      const uint32_t a01 = __byte_perm(v[4 * kk][w], v[4 * kk + 1][w], 0x5140);
-      const uint32_t a23 = __byte_perm(v[4 * kk][w], v[4 * kk + 1][w], 0x7362);
-      const uint32_t b01 = __byte_perm(v[4 * kk + 2][w], v[4 * kk + 3][w], 0x5140);
-      const uint32_t b23 = __byte_perm(v[4 * kk + 2][w], v[4 * kk + 3][w], 0x7362);
-      mma_f16(o[4 * w], p[kk], e4m3_lo(a01), e4m3_lo(b01));
-      mma_f16(o[4 * w + 1], p[kk], e4m3_hi(a01), e4m3_hi(b01));
-      mma_f16(o[4 * w + 2], p[kk], e4m3_lo(a23), e4m3_lo(b23));
-      mma_f16(o[4 * w + 3], p[kk], e4m3_hi(a23), e4m3_hi(b23));
-    }
+  for (int w = 0; w < VW; ++w) pv_words<VW, QT>(p, v, w, o + 2 * w);
 }
 
 // Channel of the first of the four codes in word i of a lane's row piece, for
@@ -142,435 +192,710 @@ __device__ __forceinline__ int factor_channel(int i, int t) {
   return t * (C / 4) + i * 4;
 }
 
-// A rows x C matrix of bf16 as fp16 A fragments, each row times 2^(14 - e) with
-// e its exponent; back[] undoes it.
+// One query row of C bf16 channels (lane g's, its t-th pieces) as fp16 B
+// fragments, times 2^(14 - e) with e the exponent of its largest; returns 2^(e - 14).
 template <int C, bool FACTOR>
-__device__ __forceinline__ void load_rows(const __nv_bfloat16* x, int stride, const bool* live,
-                                          int t, uint32_t (*frag)[4], float* back) {
-  float f[2][C / 4];
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    float top = 0.f;
-#pragma unroll
-    for (int i = 0; i < C / 16; ++i) {
-      const int ch = FACTOR ? factor_channel<C>(i, t) : piece_channel<C>(i, t);
-      uint2 v = make_uint2(0, 0);
-      if (live[half] && ch < stride)
-        v = __ldg(reinterpret_cast<const uint2*>(x + static_cast<long long>(half) * 8 * stride + ch));
-      const float e[4] = {__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u),
-                          __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u)};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        f[half][4 * i + k] = e[k];
-        top = fmaxf(top, fabsf(e[k]));
-      }
-    }
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    // exponent held so that 2^(14 - e) and its inverse are normal
-    const int e = min(max(__float_as_int(top) >> 23, 60), 194) - 127;
-    const float to = pow2f(14 - e);
-    back[half] = pow2f(e - 14);
-#pragma unroll
-    for (int i = 0; i < C / 4; ++i) f[half][i] *= to;
-  }
+__device__ __forceinline__ float load_row(const __nv_bfloat16* x, int channels, bool live, int t,
+                                          uint32_t (*frag)[2]) {
+  float f[C / 4], top = 0.f;
 #pragma unroll
   for (int i = 0; i < C / 16; ++i) {
-    frag[i][0] = pack_f16x2(f[0][4 * i], f[0][4 * i + 1]);
-    frag[i][1] = pack_f16x2(f[1][4 * i], f[1][4 * i + 1]);
-    frag[i][2] = pack_f16x2(f[0][4 * i + 2], f[0][4 * i + 3]);
-    frag[i][3] = pack_f16x2(f[1][4 * i + 2], f[1][4 * i + 3]);
+    const int ch = FACTOR ? factor_channel<C>(i, t) : piece_channel<C>(i, t);
+    uint2 v = make_uint2(0, 0);
+    if (live && ch < channels) v = __ldg(reinterpret_cast<const uint2*>(x + ch));
+    const float e[4] = {__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u),
+                        __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u)};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      f[4 * i + k] = e[k];
+      top = fmaxf(top, fabsf(e[k]));
+    }
+  }
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  // exponent held so that 2^(14 - e) and its inverse are normal
+  const int e = min(max(__float_as_int(top) >> 23, 60), 194) - 127;
+  const float to = pow2f(14 - e);
+#pragma unroll
+  for (int i = 0; i < C / 16; ++i) {
+    frag[i][0] = pack_f16x2(f[4 * i] * to, f[4 * i + 1] * to);
+    frag[i][1] = pack_f16x2(f[4 * i + 2] * to, f[4 * i + 3] * to);
+  }
+  return pow2f(e - 14);
+}
+
+// ------------------------------------------------------------------ pipeline
+// Shared memory of a CTA: barriers, the warps' (max, sum), then the ring: for
+// each of the wts token groups `stages` stages of one block, K | V | W as they
+// lie in global memory.
+constexpr int kCaMaxStages = 8;
+constexpr int kCaRing = 2048;  // offset of the ring
+
+struct CaHead {
+  uint64_t full[kCaWarps][kCaMaxStages];
+  uint64_t empty[kCaWarps][kCaMaxStages];
+  float2 ml[kCaWarps][16];
+  uint32_t held[kCaWarps];
+  int abort_flag, drain_flag;
+};
+static_assert(sizeof(CaHead) <= kCaRing, "");
+
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+
+// Column n of an 8-token tile is token (n & ~1) + ((n ^ n / 2) & 1): pairs of
+// columns keep rows of both parities, so the 64-byte rows that lanes read
+// together fall into different banks for K and for V.
+__device__ __forceinline__ int tile_token(int n) { return (n & ~1) + ((n ^ (n >> 1)) & 1); }
+
+// Token (of the block) of piece i of a lane in 16-token step kk.
+__device__ __forceinline__ int piece_token(int kk, int i, int t) {
+  return 16 * kk + 8 * (i / 2) + tile_token(2 * t + (i & 1));
+}
+// The lane's pieces of V in step kk; vrow is the block's first row at the lane's channels.
+template <int D>
+__device__ __forceinline__ void load_v(uint32_t (*v)[D / 32], uint32_t vrow, int kk, int t) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t p = vrow + piece_token(kk, i, t) * D;
+    if constexpr (D == 128) {
+      const uint4 x = ld_shared_v4(p);
+      v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+    } else if constexpr (D == 64) {
+      const uint2 x = lds64(p);
+      v[i][0] = x.x, v[i][1] = x.y;
+    } else {
+      v[i][0] = lds32(p);
+    }
   }
 }
 
-template <int D>
-struct CaSmem {
-  float o[kCaWarps][16][D + 4];
-  float2 ml[kCaWarps][16];
-};
+// The product for a block that some query does not see whole.  Codes of no token
+// (behind L: any bytes, the NaN code among them) enter as zeros.  A NaN in a
+// token that only some queries see would reach the others through 0 x NaN: such a
+// block goes query by query, with the tokens that it does not see as zeros.
+template <int D, int QT>
+__device__ __noinline__ void pv_edge_queries(const uint32_t (*p)[QT][2], uint32_t vrow, int tok0,
+                                             const int (*lim)[2], float (*o)[QT][4]) {
+  constexpr int VW = D / 32;
+  const int lane = lane_id(), g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int q = 0; q < QT; ++q)
+#pragma unroll 1
+    for (int r = 0; r < 8; ++r) {
+      const int lim_r = __shfl_sync(0xffffffffu, r & 1 ? lim[q][1] : lim[q][0], r >> 1);
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) {
+        uint32_t pr[1][2], v[4][VW];
+        load_v<D>(v, vrow, kk, t);
+        pr[0][0] = g == r ? p[kk][q][0] : 0u;
+        pr[0][1] = g == r ? p[kk][q][1] : 0u;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (tok0 + piece_token(kk, k, t) >= lim_r)
+#pragma unroll
+            for (int w = 0; w < VW; ++w) v[k][w] = 0u;
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {
+          float c[2][1][4] = {};
+          pv_words<VW, 1>(pr, v, w, c);
+          if (t == (r >> 1))
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              if (r & 1)
+                o[2 * w + n][q][1] += c[n][0][1], o[2 * w + n][q][3] += c[n][0][3];
+              else
+                o[2 * w + n][q][0] += c[n][0][0], o[2 * w + n][q][2] += c[n][0][2];
+            }
+        }
+      }
+    }
+}
+template <int D, int QT>
+__device__ __forceinline__ void pv_edge(const uint32_t (*p)[QT][2], uint32_t vrow, int tok0, int L,
+                                        const int (*lim)[2], int causal, float (*o)[QT][4]) {
+  constexpr int VW = D / 32;
+  const int t = lane_id() & 3;
+  uint32_t nan = 0;
+#pragma unroll
+  for (int kk = 0; kk < 2; ++kk) {
+    uint32_t v[4][VW];
+    load_v<D>(v, vrow, kk, t);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int w = 0; w < VW; ++w)
+        if (tok0 + piece_token(kk, i, t) < L) nan |= __vcmpeq4(v[i][w] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+  }
+  if (causal && __any_sync(0xffffffffu, nan != 0)) {
+    float c[D / 16][QT][4] = {};
+    uint32_t pc[2][QT][2];
+    int lc[QT][2];
+#pragma unroll
+    for (int q = 0; q < QT; ++q)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        pc[0][q][k] = p[0][q][k], pc[1][q][k] = p[1][q][k];
+        lc[q][k] = lim[q][k];
+      }
+    pv_edge_queries<D, QT>(pc, vrow, tok0, lc, c);
+#pragma unroll
+    for (int n = 0; n < D / 16; ++n)
+#pragma unroll
+      for (int q = 0; q < QT; ++q)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[n][q][k] += c[n][q][k];
+    return;
+  }
+#pragma unroll
+  for (int kk = 0; kk < 2; ++kk) {
+    uint32_t v[4][VW];
+    load_v<D>(v, vrow, kk, t);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (tok0 + piece_token(kk, i, t) >= L)
+#pragma unroll
+        for (int w = 0; w < VW; ++w) v[i][w] = 0u;
+    pv_step<VW, QT>(p[kk], v, o);
+  }
+}
 
-template <int D, int RP, bool MASS>
-__global__ void __launch_bounds__(kCaThreads, D == 128 ? 2 : 3)
+// QT: tiles of 8 queries a warp holds.
+template <int D, int RP, int QT, bool MASS>
+__global__ void __launch_bounds__(kCaThreads, 3)
     cache_attn_kernel(const CacheAttnArgs a) {
-  constexpr int KW = D / 16;                  // K words of a lane and 8-token tile; QK steps
+  constexpr int KW = D / 16;                  // K words of a lane and token; QK steps
   constexpr int WW = RP / 16;                 // the same for the factors
   constexpr int VW = D / 32;                  // V words of a lane and token
-  constexpr int NT = D / 8;                   // channel tiles of the PV product
-  __shared__ CaSmem<D> sm;
-  grid_dep_wait();
+  constexpr int NT = D / 16;                  // channel tiles of the PV product
+  constexpr int QR = 8 * QT;                  // queries of a warp
+  extern __shared__ __align__(1024) unsigned char smem[];
+  CaHead& head = *reinterpret_cast<CaHead*>(smem);
   const int lane = lane_id(), warp = warp_id();
   const int g = lane >> 2, t = lane & 3;
   const int wr = warp % a.wr, wt = warp / a.wr, wts = kCaWarps / a.wr;
+  const int stages = a.stages;
+  const uint32_t v_off = kCacheBlock * D, w_off = 2 * kCacheBlock * D;
+  const uint32_t w_bytes = RP > 0 ? kCacheBlock * a.r : 0, stage_bytes = w_off + w_bytes;
+  const uint32_t ring = smem_u32(smem) + kCaRing + wt * stages * stage_bytes;
+  const uint32_t full = smem_u32(&head.full[wt][0]), empty = smem_u32(&head.empty[wt][0]);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kCaWarps * kCaMaxStages; ++i) {
+      mbar_init(smem_u32(&head.full[0][0]) + 8 * i, 1);
+      mbar_init(smem_u32(&head.empty[0][0]) + 8 * i, a.wr);
+    }
+    head.abort_flag = head.drain_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const WaitGuard guard{&head.abort_flag, a.err_word, a.wait_ns, a.fail_site};
+  grid_dep_wait();
   const int mult = a.Hk * a.row_segs;
-  const long long W = blocks_before(a, a.B) * mult;
-  long long at = W * blockIdx.x / gridDim.x;
-  const long long stop = W * (blockIdx.x + 1) / gridDim.x;
+  const Place place = place_of(a, mult);
   grid_dep_launch_next();
+  unsigned at = place.at;
+  const unsigned stop = place.stop;
   if (at >= stop) return;
-  long long before;
-  int b = sequence_of(a, at / mult, before);
-  int nb = cache_blocks(a, b);
-  long long in_seq = at - before * mult;  // position inside sequence b's segments
-  int seg = static_cast<int>(in_seq / nb);
-  int blk0 = static_cast<int>(in_seq - static_cast<long long>(seg) * nb);
-  const int seg_rows = min(a.R, 16 * a.wr);
-  bool first = true;
+  int b = place.b, nb = place.nb, seg = place.seg, blk0 = place.blk;
+  int blk1 = static_cast<int>(min(static_cast<unsigned>(nb), blk0 + (stop - at)));
+  const int seg_rows = min(a.R, QR * a.wr);
+  bool first = true, dead = false;
+  const bool leader = wr == 0;
+  // ring position of the next block to load and to use, and its phase
+  int in_stage = 0, in_phase = 0, out_stage = 0, out_phase = 0;
+  int loads = 0;   // copies this warp started (the ring's s-th stage got loads s, s + stages, ...)
+  int issued = 0;  // blocks of this segment (and the next) loaded by this group so far
 
   while (at < stop) {
     const int h = seg / a.row_segs, rs = seg - h * a.row_segs;
-    const int blk1 = static_cast<int>(min(static_cast<long long>(nb), blk0 + (stop - at)));
     const int L = min(a.lengths[b], a.cap);
     const long long bh = static_cast<long long>(b) * a.Hk + h;
-    const int row0 = (rs * a.wr + wr) * 16;
-
-    // rows g and g + 8 of this warp's tile
-    bool live[2];
-    int lim[2];  // tokens the row sees
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int row = row0 + g + 8 * i;
-      live[i] = row < a.R;
-      lim[i] = L;
-      if (a.causal && live[i]) lim[i] = max(min(L, L - a.Nq + 1 + row % a.Nq), 0);
+    const int row0 = (rs * a.wr + wr) * QR;
+    // the segment after this one
+    const unsigned next_at = at + (blk1 - blk0);
+    int nseg = seg + 1, nxb = b, nnb = nb;
+    if (nseg == mult) {
+      nseg = 0;
+      do {
+        ++nxb;
+      } while (nxb < a.B && cache_blocks(a, nxb) == 0);
+      if (nxb < a.B) nnb = cache_blocks(a, nxb);
     }
-    const int lim_lo = __reduce_min_sync(0xffffffffu, min(lim[0], lim[1]));
+    const int nblk1 =
+        next_at < stop ? static_cast<int>(min(static_cast<unsigned>(nnb), stop - next_at)) : 0;
+    const int mine = (blk1 - blk0 - wt + wts - 1) / wts;           // this group's blocks here
+    const int ahead = mine + (nblk1 - wt + wts - 1) / wts;         // and with the next segment's
+    const long long nbh = static_cast<long long>(nxb) * a.Hk + nseg / a.row_segs;
 
-    uint32_t qf[KW][4];
-    float fq[2];
-    load_rows<D, false>(a.q + (bh * a.R + row0 + g) * D, D, live, t, qf, fq);
-    fq[0] *= a.scale_log2;
-    fq[1] *= a.scale_log2;
-    uint32_t uf[WW > 0 ? WW : 1][4];
-    float fu[2] = {0.f, 0.f};
-    if constexpr (RP > 0) {
-      load_rows<RP, true>(a.u + (bh * a.R + row0 + g) * a.r, a.r, live, t, uf, fu);
-      fu[0] *= kLog2e;
-      fu[1] *= kLog2e;
+    // Loads blocks until `upto` of them (counted from this segment's first) are under way.
+    const auto pump = [&](int upto) {
+      while (issued < min(upto, ahead)) {
+        if (leader && !dead) {
+          const bool here = issued < mine;
+          const long long tok =
+              (here ? bh : nbh) * a.cap +
+              static_cast<long long>(here ? blk0 + wt + issued * wts : wt + (issued - mine) * wts) *
+                  kCacheBlock;
+          bool ok = true;
+          if (a.wr > 1) ok = wait_warp(empty + 8 * in_stage, in_phase ^ 1, guard, 70);
+          if (!ok) dead = true;
+          if (ok && lane == 0) {
+            const uint32_t bar = full + 8 * in_stage, dst = ring + in_stage * stage_bytes;
+            mbar_expect_tx(bar, stage_bytes);
+            bulk_load(dst, a.k + tok * D, v_off, bar);
+            bulk_load(dst + v_off, a.v + tok * D, v_off, bar);
+            if constexpr (RP > 0) bulk_load(dst + w_off, a.w + tok * a.r, w_bytes, bar);
+          }
+          loads += ok;
+        }
+        if (++in_stage == stages) in_stage = 0, in_phase ^= 1;
+        ++issued;
+      }
+    };
+    pump(stages);
+
+    // Queries as B fragments (lane g: query g of each tile); scores, sums and O are
+    // held for queries 2 t, 2 t + 1.
+    uint32_t qf[QT][KW][2], uf[QT][WW > 0 ? WW : 1][2];
+    float fq[QT][2], fu[QT][2];
+    int lim[QT][2], lim_lo = L;  // tokens the query sees
+#pragma unroll
+    for (int q = 0; q < QT; ++q) {
+      const int row = row0 + 8 * q + g;
+      const float f = load_row<D, false>(a.q + (bh * a.R + row) * D, D, row < a.R, t, qf[q]) *
+                      a.scale_log2;
+      float e = 0.f;
+      if constexpr (RP > 0)
+        e = load_row<RP, true>(a.u + (bh * a.R + row) * a.r, a.r, row < a.R, t, uf[q]) * kLog2e;
+      int n = L;
+      if (a.causal && row < a.R) n = max(min(L, L - a.Nq + 1 + row % a.Nq), 0);
+      lim_lo = min(lim_lo, n);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int from = 4 * (2 * t + k);
+        fq[q][k] = __shfl_sync(0xffffffffu, f, from);
+        fu[q][k] = __shfl_sync(0xffffffffu, e, from);
+        lim[q][k] = __shfl_sync(0xffffffffu, n, from);
+      }
     }
+    lim_lo = __reduce_min_sync(0xffffffffu, lim_lo);
 
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    float oacc[NT][4];
+    float m[QT][2], l[QT][2], oacc[NT][QT][4];
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int q = 0; q < QT; ++q) {
+      m[q][0] = m[q][1] = -INFINITY;
+      l[q][0] = l[q][1] = 0.f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) oacc[i][k] = 0.f;
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) oacc[i][q][k] = 0.f;
+    }
     float unit = 1.f;  // oacc is O / unit
 
-    const uint8_t* kp = a.k + bh * a.cap * D;
-    const uint8_t* vp = a.v + bh * a.cap * D;
-    const uint8_t* wp = RP > 0 ? a.w + bh * a.cap * a.r : nullptr;
     const long long sbase = bh * (a.cap / kCacheBlock);
-    uint32_t kr[4][KW], vr[8][VW], wreg[4][WW > 0 ? WW : 1];
     float ksc = 1.f, vsc = 1.f, wsc = 0.f;
+    const auto load_scales = [&](int blk) {
+      ksc = __ldg(a.ks + sbase + blk);
+      vsc = __ldg(a.vs + sbase + blk);
+      if constexpr (RP > 0) wsc = __ldg(a.ws + sbase + blk);
+    };
+    if (mine > 0) load_scales(blk0 + wt);
+    uint32_t held = 0;  // stage of the segment's last block: the warps join through it
 
-    const auto load_k = [&](int blk) {
+    for (int i = 0; i < mine; ++i) {
+      const int blk = blk0 + wt + i * wts;
+      if (!wait_warp(full + 8 * out_stage, out_phase, guard, 71)) dead = true;
+      const uint32_t st = ring + out_stage * stage_bytes;
+      const float ks_now = ksc, vs_now = vsc, ws_now = wsc;
+      if (i + 1 < mine) load_scales(blk + wts);
+      // scores in units of log2: x[j][q] of tokens g, g + 8 of half j (as tile_token
+      // orders them) and queries 2 t, 2 t + 1
+      float x[2][QT][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint8_t* p = kp + (static_cast<long long>(blk) * kCacheBlock + 8 * j + g) * D;
-        if constexpr (D >= 64) {
+      for (int j = 0; j < 2; ++j) {
+        uint32_t kr[2][KW];
 #pragma unroll
-          for (int c = 0; c < KW / 4; ++c) {
-            const uint4 x = __ldg(reinterpret_cast<const uint4*>(p + 64 * c + 16 * t));
-            kr[j][4 * c] = x.x, kr[j][4 * c + 1] = x.y, kr[j][4 * c + 2] = x.z, kr[j][4 * c + 3] = x.w;
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t p = st + (16 * j + 8 * e + tile_token(g)) * D;
+          if constexpr (D >= 64) {
+#pragma unroll
+            for (int c = 0; c < KW / 4; ++c) {
+              const uint4 v = ld_shared_v4(p + 64 * c + 16 * t);
+              kr[e][4 * c] = v.x, kr[e][4 * c + 1] = v.y;
+              kr[e][4 * c + 2] = v.z, kr[e][4 * c + 3] = v.w;
+            }
+          } else {
+            const uint2 v = lds64(p + 8 * t);
+            kr[e][0] = v.x, kr[e][1] = v.y;
           }
-        } else {
-          const uint2 x = __ldg(reinterpret_cast<const uint2*>(p + 8 * t));
-          kr[j][0] = x.x, kr[j][1] = x.y;
+        }
+#pragma unroll
+        for (int q = 0; q < QT; ++q)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[j][q][k] = 0.f;
+#pragma unroll
+        for (int k = 0; k < KW; ++k) {
+          const uint32_t af[4] = {e4m3_lo(kr[0][k]), e4m3_lo(kr[1][k]), e4m3_hi(kr[0][k]),
+                                  e4m3_hi(kr[1][k])};
+#pragma unroll
+          for (int q = 0; q < QT; ++q) mma_f16(x[j][q], af, qf[q][k][0], qf[q][k][1]);
         }
         if constexpr (RP > 0) {
-          const uint8_t* pw = wp + (static_cast<long long>(blk) * kCacheBlock + 8 * j + g) * a.r;
+          uint32_t wreg[2][WW];
 #pragma unroll
-          for (int i = 0; i < WW; ++i) wreg[j][i] = 0;
-          if constexpr (RP == 16) {
-            if (4 * t < a.r) wreg[j][0] = __ldg(reinterpret_cast<const uint32_t*>(pw + 4 * t));
-          } else {
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t pw = st + w_off + (16 * j + 8 * e + tile_token(g)) * a.r;
 #pragma unroll
-            for (int c = 0; c < WW / 2; ++c) {
-              const int ch = factor_channel<RP>(2 * c, t);
-              if (ch < a.r) {
-                const uint2 x = __ldg(reinterpret_cast<const uint2*>(pw + ch));
-                wreg[j][2 * c] = x.x, wreg[j][2 * c + 1] = x.y;
+            for (int k = 0; k < WW; ++k) wreg[e][k] = 0;
+            if constexpr (RP == 16) {
+              if (4 * t < a.r) wreg[e][0] = lds32(pw + 4 * t);
+            } else {
+#pragma unroll
+              for (int k = 0; k < WW / 2; ++k) {
+                const int ch = factor_channel<RP>(2 * k, t);
+                if (ch < a.r) {
+                  const uint2 v = lds64(pw + ch);
+                  wreg[e][2 * k] = v.x, wreg[e][2 * k + 1] = v.y;
+                }
               }
             }
           }
-        }
-      }
-      ksc = __ldg(a.ks + sbase + blk);
-      if constexpr (RP > 0) wsc = __ldg(a.ws + sbase + blk);
-    };
-    // token 16 kk + 8 (i / 2) + 2 t + i % 2 of the block is vr[4 kk + i]
-    const auto load_v = [&](int blk) {
+          float cw[QT][4] = {};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int tok = 16 * (i / 4) + 8 * ((i / 2) & 1) + 2 * t + (i & 1);
-        const uint8_t* p = vp + (static_cast<long long>(blk) * kCacheBlock + tok) * D + g * (D / 8);
-        if constexpr (D == 128) {
-          const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
-          vr[i][0] = x.x, vr[i][1] = x.y, vr[i][2] = x.z, vr[i][3] = x.w;
-        } else if constexpr (D == 64) {
-          const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
-          vr[i][0] = x.x, vr[i][1] = x.y;
+          for (int k = 0; k < WW; ++k) {
+            const uint32_t af[4] = {e4m3_lo(wreg[0][k]), e4m3_lo(wreg[1][k]), e4m3_hi(wreg[0][k]),
+                                    e4m3_hi(wreg[1][k])};
+#pragma unroll
+            for (int q = 0; q < QT; ++q) mma_f16(cw[q], af, uf[q][k][0], uf[q][k][1]);
+          }
+#pragma unroll
+          for (int q = 0; q < QT; ++q)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              x[j][q][k] = fmaf(cw[q][k], fu[q][k & 1] * ws_now, x[j][q][k] * (fq[q][k & 1] * ks_now));
         } else {
-          vr[i][0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+#pragma unroll
+          for (int q = 0; q < QT; ++q)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[j][q][k] *= fq[q][k & 1] * ks_now;
         }
       }
-      vsc = __ldg(a.vs + sbase + blk);
-    };
-
-    int blk = blk0 + wt;
-    if (blk < blk1) {
-      load_k(blk);
-      load_v(blk);
-    }
-    for (; blk < blk1; blk += wts) {
-      // scores of 16 rows x 32 tokens, in units of log2
-      float x[4][4];
-      const float f0 = fq[0] * ksc, f1 = fq[1] * ksc;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < KW; ++i) mma_f16(c, qf[i], e4m3_lo(kr[j][i]), e4m3_hi(kr[j][i]));
-        x[j][0] = c[0] * f0, x[j][1] = c[1] * f0, x[j][2] = c[2] * f1, x[j][3] = c[3] * f1;
-        if constexpr (RP > 0) {
-          float cw[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int i = 0; i < WW; ++i) mma_f16(cw, uf[i], e4m3_lo(wreg[j][i]), e4m3_hi(wreg[j][i]));
-          x[j][0] = fmaf(cw[0], fu[0] * wsc, x[j][0]);
-          x[j][1] = fmaf(cw[1], fu[0] * wsc, x[j][1]);
-          x[j][2] = fmaf(cw[2], fu[1] * wsc, x[j][2]);
-          x[j][3] = fmaf(cw[3], fu[1] * wsc, x[j][3]);
-        }
-      }
-      const bool edge = (blk + 1) * kCacheBlock > lim_lo;  // a row does not see all of the block
-      if (blk + wts < blk1) load_k(blk + wts);
+      const bool edge = (blk + 1) * kCacheBlock > lim_lo;  // a query does not see all of the block
       if (edge) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int tok = blk * kCacheBlock + 8 * j + 2 * t + (k & 1);
-            if (tok >= lim[k >> 1]) x[j][k] = -INFINITY;
-          }
-        // codes of no token (any bytes, the NaN code among them) do not enter the product
+          for (int q = 0; q < QT; ++q)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int tok = 16 * (i / 4) + 8 * ((i / 2) & 1) + 2 * t + (i & 1);
-          if (blk * kCacheBlock + tok >= L)
-#pragma unroll
-            for (int k = 0; k < VW; ++k) vr[i][k] = 0;
-        }
+            for (int k = 0; k < 4; ++k)
+              if (blk * kCacheBlock + 16 * j + 8 * (k >> 1) + tile_token(g) >= lim[q][k & 1])
+                x[j][q][k] = -INFINITY;
       }
       if constexpr (MASS) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (live[i]) {
-            float* s = a.scores + (bh * a.R + row0 + g + 8 * i) * a.cap + blk * kCacheBlock + 2 * t;
+        for (int q = 0; q < QT; ++q)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              *reinterpret_cast<float2*>(s + 8 * j) = make_float2(x[j][2 * i], x[j][2 * i + 1]);
+          for (int e = 0; e < 2; ++e) {
+            const int row = row0 + 8 * q + 2 * t + e;
+            if (row < a.R) {
+              float* s = a.scores + (bh * a.R + row) * a.cap + blk * kCacheBlock + tile_token(g);
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                s[16 * j] = x[j][q][e], s[16 * j + 8] = x[j][q][2 + e];
+            }
           }
       }
       // running maximum and sum
-      float mx[2];
+      float mx[QT][2];
+      bool moved = vs_now != unit;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float v = m[i];
+      for (int q = 0; q < QT; ++q)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v = fmax3(v, x[j][2 * i], x[j][2 * i + 1]);
-        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-        mx[i] = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-      }
-      const bool moved = mx[0] != m[0] || mx[1] != m[1] || vsc != unit;
+        for (int e = 0; e < 2; ++e) {
+          float v = fmax3(m[q][e], x[0][q][e], x[0][q][2 + e]);
+          v = fmax3(v, x[1][q][e], x[1][q][2 + e]);
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+          mx[q][e] = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+          moved |= mx[q][e] != m[q][e];
+        }
       if (__any_sync(0xffffffffu, moved)) {
-        const float back = unit / vsc;
-        unit = vsc;
-        float al[2];
+        const float back = unit / vs_now;
+        unit = vs_now;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          al[i] = mx[i] == -INFINITY ? 1.f : fast_exp2(m[i] - mx[i]);
-          m[i] = mx[i];
-          l[i] *= al[i];
-          al[i] *= back;
-        }
+        for (int q = 0; q < QT; ++q) {
+          float al[2];
 #pragma unroll
-        for (int k = 0; k < NT; ++k) {
-          oacc[k][0] *= al[0], oacc[k][1] *= al[0];
-          oacc[k][2] *= al[1], oacc[k][3] *= al[1];
-        }
-      }
-      const float base[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          x[j][k] = fast_exp2(x[j][k] - base[k >> 1]);
-          l[k >> 1] += x[j][k];
-        }
-      // O += P V
-      uint32_t p[2][4];
-#pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
-        p[kk][0] = pack_f16x2(x[2 * kk][0], x[2 * kk][1]);
-        p[kk][1] = pack_f16x2(x[2 * kk][2], x[2 * kk][3]);
-        p[kk][2] = pack_f16x2(x[2 * kk + 1][0], x[2 * kk + 1][1]);
-        p[kk][3] = pack_f16x2(x[2 * kk + 1][2], x[2 * kk + 1][3]);
-      }
-      bool poison = false;  // a NaN in V that some rows may not see
-      if (edge && a.causal) {
-        uint32_t any = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-          for (int k = 0; k < VW; ++k) any |= __vcmpeq4(vr[i][k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-        poison = __any_sync(0xffffffffu, any != 0);
-      }
-      if (!poison) {
-        pv_product<VW>(p, vr, oacc);
-      } else {
-        // 0 x NaN is NaN, so a masked weight does not keep it out: row by row,
-        // with the tokens that the row does not see as zeros
-#pragma unroll 1
-        for (int r = 0; r < 16; ++r) {
-          const int lim_r = __shfl_sync(0xffffffffu, r < 8 ? lim[0] : lim[1], (r & 7) * 4);
-          const bool mine = g == (r & 7);
-          uint32_t pr[2][4], vm[8][VW];
-          float c[NT][4];
-#pragma unroll
-          for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) pr[kk][k] = mine && (k & 1) == (r >> 3) ? p[kk][k] : 0u;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int tok = 16 * (i / 4) + 8 * ((i / 2) & 1) + 2 * t + (i & 1);
-#pragma unroll
-            for (int k = 0; k < VW; ++k)
-              vm[i][k] = blk * kCacheBlock + tok < lim_r ? vr[i][k] : 0u;
+          for (int e = 0; e < 2; ++e) {
+            al[e] = mx[q][e] == -INFINITY ? 1.f : fast_exp2(m[q][e] - mx[q][e]);
+            m[q][e] = mx[q][e];
+            l[q][e] *= al[e];
+            al[e] *= back;
           }
 #pragma unroll
-          for (int i = 0; i < NT; ++i)
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) c[i][k] = 0.f;
-          pv_product<VW>(pr, vm, c);
-          if (mine) {
+            for (int k = 0; k < 4; ++k) oacc[n][q][k] *= al[k & 1];
+        }
+      }
+      uint32_t p[2][QT][2];
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-              oacc[i][0] += r < 8 ? c[i][0] : 0.f, oacc[i][1] += r < 8 ? c[i][1] : 0.f;
-              oacc[i][2] += r < 8 ? 0.f : c[i][2], oacc[i][3] += r < 8 ? 0.f : c[i][3];
+      for (int q = 0; q < QT; ++q) {
+        const float base[2] = {m[q][0] == -INFINITY ? 0.f : m[q][0],
+                               m[q][1] == -INFINITY ? 0.f : m[q][1]};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            x[j][q][k] = fast_exp2(x[j][q][k] - base[k & 1]);
+            l[q][k & 1] += x[j][q][k];
+          }
+          p[j][q][0] = transpose8x8(pack_f16x2(x[j][q][0], x[j][q][1]));
+          p[j][q][1] = transpose8x8(pack_f16x2(x[j][q][2], x[j][q][3]));
+        }
+      }
+      // O^T += V^T P^T
+      const uint32_t vrow = st + v_off + g * (D / 8);
+      if (!edge) {
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+          uint32_t v[4][VW];
+          load_v<D>(v, vrow, kk, t);
+          pv_step<VW, QT>(p[kk], v, oacc);
+        }
+      } else {
+        pv_edge<D, QT>(p, vrow, blk * kCacheBlock, L, lim, a.causal, oacc);
+      }
+      held = st;
+      __syncwarp();  // the stage has been read
+      if (a.wr > 1 && lane == 0 && i + 1 < mine) mbar_arrive(empty + 8 * out_stage);
+      if (i + 1 < mine) {
+        if (++out_stage == stages) out_stage = 0, out_phase ^= 1;
+        pump(i + 1 + stages);
+      }
+    }
+
+    // Join the warps that share rows: the groups behind the first leave O in a
+    // stage that is read out (tile wr in that of group wr, or their own), the
+    // first adds them to its own.  Channel g (D / 8) + 2 n + i of query 2 t + e is
+    // oacc[n][q][2 i + e].
+#pragma unroll
+    for (int q = 0; q < QT; ++q) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) l[q][e] += __shfl_xor_sync(0xffffffffu, l[q][e], o);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) oacc[n][q][k] *= unit;
+    }
+    const bool whole = blk0 == 0 && blk1 == nb;
+    const int slot = first ? 0 : 1;
+    if (wts > 1) {
+      if (lane == 0 && wr == 0) head.held[wt] = mine > 0 ? held : 0u;
+      if (g == 0) {
+#pragma unroll
+        for (int q = 0; q < QT; ++q)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            head.ml[warp][8 * q + 2 * t + e] = make_float2(m[q][e], l[q][e]);
+      }
+      __syncthreads();
+      const uint32_t buf = head.held[a.wr == 1 ? wt : wr];
+      if (wt > 0 && mine > 0) {
+#pragma unroll
+        for (int q = 0; q < QT; ++q)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            st_shared_v4(buf + ((q * NT + n) * 32 + lane) * 16, __float_as_uint(oacc[n][q][0]),
+                         __float_as_uint(oacc[n][q][1]), __float_as_uint(oacc[n][q][2]),
+                         __float_as_uint(oacc[n][q][3]));
+      }
+      __syncthreads();
+      if (wt == 0) {
+#pragma unroll
+        for (int q = 0; q < QT; ++q) {
+          float mm[2] = {m[q][0], m[q][1]}, base[2], f[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            for (int w = 1; w < wts; ++w)
+              mm[e] = fmaxf(mm[e], head.ml[w * a.wr + wr][8 * q + 2 * t + e].x);
+            base[e] = mm[e] == -INFINITY ? 0.f : mm[e];
+            f[e] = fast_exp2(m[q][e] - base[e]);
+            l[q][e] *= f[e];
+            m[q][e] = mm[e];
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) oacc[n][q][k] *= f[k & 1];
+          for (int w = 1; w < wts; ++w) {
+            if (blk0 + w >= blk1) break;  // groups from here on had no block
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float2 ml = head.ml[w * a.wr + wr][8 * q + 2 * t + e];
+              f[e] = fast_exp2(ml.x - base[e]);
+              l[q][e] = fmaf(ml.y, f[e], l[q][e]);
+            }
+            const uint32_t from = head.held[a.wr == 1 ? w : wr];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              const uint4 v = ld_shared_v4(from + ((q * NT + n) * 32 + lane) * 16);
+              oacc[n][q][0] = fmaf(__uint_as_float(v.x), f[0], oacc[n][q][0]);
+              oacc[n][q][1] = fmaf(__uint_as_float(v.y), f[1], oacc[n][q][1]);
+              oacc[n][q][2] = fmaf(__uint_as_float(v.z), f[0], oacc[n][q][2]);
+              oacc[n][q][3] = fmaf(__uint_as_float(v.w), f[1], oacc[n][q][3]);
             }
           }
         }
       }
-      if (blk + wts < blk1) load_v(blk + wts);
     }
-
-    // join the warps that share rows: channel 2 t (D / 8) + i of a row is oacc[i][0],
-    // the next D / 8 oacc[i][1]
+    if (wt == 0) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-      if (t == 0) sm.ml[warp][g + 8 * i] = make_float2(m[i], l[i]);
+      for (int q = 0; q < QT; ++q)
 #pragma unroll
-      for (int k = 0; k < NT; k += 4)
+        for (int e = 0; e < 2; ++e) {
+          const int row = row0 + 8 * q + 2 * t + e;
+          if (row >= a.R) continue;
+          if (whole) {
+            // no token seen: O = 0; NaN stays
+            const float inv = l[q][e] > 0.f ? 1.f / l[q][e] : l[q][e];
+            const long long out = bh * a.R + row;
+            uint32_t w[NT];
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          *reinterpret_cast<float4*>(&sm.o[warp][g + 8 * i][(2 * t + e) * NT + k]) =
-              make_float4(oacc[k][2 * i + e] * unit, oacc[k + 1][2 * i + e] * unit,
-                          oacc[k + 2][2 * i + e] * unit, oacc[k + 3][2 * i + e] * unit);
+            for (int n = 0; n < NT; ++n)
+              w[n] = pack_bf16x2(oacc[n][q][e] * inv, oacc[n][q][2 + e] * inv);
+            uint32_t* o = reinterpret_cast<uint32_t*>(a.o + out * D + g * (D / 8));
+            if constexpr (NT >= 4) {
+#pragma unroll
+              for (int n = 0; n < NT; n += 4)
+                *reinterpret_cast<uint4*>(o + n) = make_uint4(w[n], w[n + 1], w[n + 2], w[n + 3]);
+            } else {
+              *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
+            }
+            if (g == 0) a.lse[out] = (m[q][e] + __log2f(l[q][e])) * kLn2;
+          } else {
+            const long long r =
+                (static_cast<long long>(blockIdx.x) * 2 + slot) * seg_rows + (row - rs * a.wr * QR);
+            float4* o = reinterpret_cast<float4*>(a.part_o + r * D + g * (D / 8));
+#pragma unroll
+            for (int n = 0; n < NT; n += 2)
+              o[n / 2] = make_float4(oacc[n][q][e], oacc[n][q][2 + e], oacc[n + 1][q][e],
+                                     oacc[n + 1][q][2 + e]);
+            if (g == 0) a.part_ml[r] = make_float2(m[q][e], l[q][e]);
+          }
+        }
     }
-    __syncthreads();
-    const bool whole = blk0 == 0 && blk1 == nb;
-    const int slot = first ? 0 : 1;
-    for (int i = threadIdx.x; i < 16 * a.wr * (D / 4); i += kCaThreads) {
-      const int rr = i / (D / 4), c = (i - rr * (D / 4)) * 4;
-      const int row = rs * a.wr * 16 + rr;
-      if (row >= a.R) continue;
-      const int w0 = rr / 16, r16 = rr % 16;
-      float mm = -INFINITY;
-      for (int w = 0; w < wts; ++w) mm = fmaxf(mm, sm.ml[w0 + w * a.wr][r16].x);
-      const float base = mm == -INFINITY ? 0.f : mm;
-      float ll = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int w = 0; w < wts; ++w) {
-        const int ww = w0 + w * a.wr;
-        const float f = fast_exp2(sm.ml[ww][r16].x - base);
-        const float4 v = *reinterpret_cast<const float4*>(&sm.o[ww][r16][c]);
-        ll = fmaf(sm.ml[ww][r16].y, f, ll);
-        acc.x = fmaf(v.x, f, acc.x), acc.y = fmaf(v.y, f, acc.y);
-        acc.z = fmaf(v.z, f, acc.z), acc.w = fmaf(v.w, f, acc.w);
-      }
-      if (whole) {
-        const float inv = ll > 0.f ? 1.f / ll : ll;  // no token seen: O = 0; NaN stays
-        const long long out = bh * a.R + row;
-        *reinterpret_cast<uint2*>(a.o + out * D + c) =
-            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-        if (c == 0) a.lse[out] = (mm + __log2f(ll)) * kLn2;
-      } else {
-        const long long p = (static_cast<long long>(blockIdx.x) * 2 + slot) * seg_rows + rr;
-        *reinterpret_cast<float4*>(a.part_o + p * D + c) = acc;
-        if (c == 0) a.part_ml[p] = make_float2(mm, ll);
-      }
+    // the held stages go back to the ring
+    if (wts > 1) {
+      fence_async_smem();
+      __syncthreads();
     }
-    __syncthreads();
+    if (mine > 0) {
+      if (a.wr > 1 && lane == 0) mbar_arrive(empty + 8 * out_stage);
+      if (++out_stage == stages) out_stage = 0, out_phase ^= 1;
+    }
+    issued -= mine;
     first = false;
-    at += blk1 - blk0;
+    at = next_at;
+    b = nxb, seg = nseg, nb = nnb;
     blk0 = 0;
-    if (++seg == mult) {
-      seg = 0;
-      do {
-        ++b;
-      } while (b < a.B && cache_blocks(a, b) == 0);
-      if (b < a.B) nb = cache_blocks(a, b);
-    }
+    blk1 = nblk1;
+  }
+  // every copy has been waited for above, unless a wait gave up
+  if (dead && leader) {
+    const WaitGuard drain{&head.drain_flag, a.err_word, kDrainTimeoutNs, -1};
+    for (int s = 0; s < min(stages, loads); ++s)
+      wait_bounded(full + 8 * s, ((loads - 1 - s) / stages) & 1, drain, 72);
   }
 }
 
-// Joins the partials of the segments that several CTAs share and writes the
-// rows of empty sequences.  D / 4 threads a row; blockIdx.x is (b, h, row
-// segment).
+// Joins the partials of the segments that several CTAs share, in their order,
+// and writes the rows of empty sequences.  One CTA a row (blockIdx.y) of a (b, h,
+// row segment): the statistics of all partials first, then D / 4 threads a
+// partial, as many partials at once as fit.
 template <int D>
-__global__ void __launch_bounds__(128) cache_attn_combine_kernel(const CacheAttnArgs a, int ctas) {
+__global__ void __launch_bounds__(128) cache_attn_combine_kernel(const CacheAttnArgs a,
+                                                                 unsigned ctas) {
+  constexpr int TPR = D / 4, PAR = 128 / TPR;
+  __shared__ float weight[128];
+  __shared__ float4 sum[128];
+  __shared__ float s_max[4], s_l[4];
   grid_dep_wait();
-  constexpr int TPR = D / 4;
-  const int seg_rows = min(a.R, 16 * a.wr);
-  const int rr = blockIdx.y * (128 / TPR) + threadIdx.x / TPR;
-  const int c = (threadIdx.x % TPR) * 4;
+  const int seg_rows = min(a.R, a.tile * a.wr), rr = blockIdx.y;
+  const int c = (threadIdx.x % TPR) * 4, part = threadIdx.x / TPR, warp = warp_id();
   const int mult = a.Hk * a.row_segs;
   const int b = blockIdx.x / mult, seg = blockIdx.x - b * mult;
   const int h = seg / a.row_segs, rs = seg - h * a.row_segs;
-  const long long W = blocks_before(a, a.B) * mult;
-  const int nb = cache_blocks(a, b);
-  const long long s0 = blocks_before(a, b) * mult + static_cast<long long>(seg) * nb, s1 = s0 + nb;
-  const int row = rs * a.wr * 16 + rr;
-  if (rr >= seg_rows || row >= a.R) return;
+  const int row = rs * a.wr * a.tile + rr;
+  if (row >= a.R) return;
   const long long out = (static_cast<long long>(b) * a.Hk + h) * a.R + row;
+  unsigned before, total;
+  count_blocks(a, b, before, total);
+  const unsigned nb = cache_blocks(a, b);
   if (nb == 0) {
-    *reinterpret_cast<uint2*>(a.o + out * D + c) = make_uint2(0, 0);
-    if (c == 0) a.lse[out] = -INFINITY;
+    if (part == 0) *reinterpret_cast<uint2*>(a.o + out * D + c) = make_uint2(0, 0);
+    if (threadIdx.x == 0) a.lse[out] = -INFINITY;
     return;
   }
-  // CTA i holds [W i / ctas, W (i + 1) / ctas)
-  const auto start_of = [&](long long i) { return W * i / ctas; };
-  long long i0 = s0 * ctas / W;
-  while (start_of(i0 + 1) <= s0) ++i0;
-  while (start_of(i0) > s0) --i0;
-  if (start_of(i0 + 1) >= s1) return;  // one CTA had it whole
-  float m = -INFINITY, l = 0.f;
+  const unsigned s0 = before * mult + seg * nb, s1 = s0 + nb;
+  const Cut cut(total * mult, ctas);
+  const unsigned i0 = cut.holder(s0), i1 = cut.holder(s1 - 1);
+  if (i0 == i1) return;  // one CTA had it whole
+  // partial k of i0 .. i1: the CTA's first segment (slot 0), but for one that started before
+  const unsigned n = i1 - i0 + 1;
+  const unsigned late = cut.start(i0) < s0 ? 1u : 0u;
+  const auto index = [&](unsigned k) {
+    return (static_cast<long long>(i0 + k) * 2 + (k == 0 ? late : 0u)) * seg_rows + rr;
+  };
+  float m = -INFINITY;
+  for (unsigned k = threadIdx.x; k < n; k += 128) m = fmaxf(m, a.part_ml[index(k)].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane_id() == 0) s_max[warp] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
+  const float base = m == -INFINITY ? 0.f : m;
+  float l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (long long i = i0; i < ctas && start_of(i) < s1; ++i) {
-    if (start_of(i + 1) == start_of(i)) continue;
-    const int slot = start_of(i) >= s0 ? 0 : 1;  // the CTA's first segment, or a later one
-    const long long p = (i * 2 + slot) * seg_rows + rr;
-    const float2 ml = a.part_ml[p];
-    const float4 v = *reinterpret_cast<const float4*>(a.part_o + p * D + c);
-    const float mn = fmaxf(m, ml.x);
-    const float base = mn == -INFINITY ? 0.f : mn;
-    const float f = fast_exp2(m - base), e = fast_exp2(ml.x - base);
-    m = mn;
-    l = l * f + ml.y * e;
-    acc.x = acc.x * f + v.x * e, acc.y = acc.y * f + v.y * e;
-    acc.z = acc.z * f + v.z * e, acc.w = acc.w * f + v.w * e;
+  for (unsigned k0 = 0; k0 < n; k0 += 128) {
+    const unsigned k = k0 + threadIdx.x;
+    if (k < n) {
+      const float2 ml = a.part_ml[index(k)];
+      const float f = fast_exp2(ml.x - base);
+      weight[threadIdx.x] = f;
+      l = fmaf(ml.y, f, l);
+    }
+    __syncthreads();
+    const unsigned top = min(128u, n - k0);
+#pragma unroll 4
+    for (unsigned j = part; j < top; j += PAR) {
+      const float f = weight[j];
+      const float4 v = *reinterpret_cast<const float4*>(a.part_o + index(k0 + j) * D + c);
+      acc.x = fmaf(v.x, f, acc.x), acc.y = fmaf(v.y, f, acc.y);
+      acc.z = fmaf(v.z, f, acc.z), acc.w = fmaf(v.w, f, acc.w);
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (lane_id() == 0) s_l[warp] = l;
+  sum[threadIdx.x] = acc;
+  __syncthreads();
+  if (part != 0) return;
+  l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
+  for (int p = 1; p < PAR; ++p) {
+    const float4 v = sum[threadIdx.x + p * TPR];
+    acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
   }
   const float inv = l > 0.f ? 1.f / l : l;
   *reinterpret_cast<uint2*>(a.o + out * D + c) =

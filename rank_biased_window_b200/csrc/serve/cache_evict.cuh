@@ -190,7 +190,7 @@ __device__ __forceinline__ void move_rows(const uint8_t* from, const float* from
     }
 #pragma unroll
     for (int it = 0; it < ITS; ++it)
-      top = fmaxf(top, e4m3x2_to_f32x2(static_cast<uint16_t>(Piece<P>::mag(v[it]))).x * sc[it]);
+      top = fmaxf(top, f16x2_to_f32x2(e4m3_lo(Piece<P>::mag(v[it]))).x * sc[it]);
     top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
   }
   meet();

@@ -26,14 +26,18 @@ __device__ __forceinline__ float scale_for(float amax) {
   return pow2f(min(max(e, kScaleMinExp), kScaleMaxExp));
 }
 
-// Two e4m3 codes (the low 16 bits of a register) as two fp16 values; exact.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t v) {
+// Two e4m3 codes, the low or the high half of a register, as two fp16 values; exact.
+__device__ __forceinline__ uint32_t e4m3_lo(uint32_t w) {
   uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(v));
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(w));
   return r;
 }
-__device__ __forceinline__ float2 e4m3x2_to_f32x2(uint16_t v) {
-  const uint32_t h = e4m3x2_to_f16x2(v);
+__device__ __forceinline__ uint32_t e4m3_hi(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ float2 f16x2_to_f32x2(uint32_t h) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 // Round to nearest even; magnitudes above 448 become 448, NaN the NaN code.
@@ -44,8 +48,7 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
 }
 // Four codes to a scale that is 1 / ratio times theirs.
 __device__ __forceinline__ uint32_t requantise4(uint32_t v, float ratio) {
-  const float2 a = e4m3x2_to_f32x2(static_cast<uint16_t>(v));
-  const float2 b = e4m3x2_to_f32x2(static_cast<uint16_t>(v >> 16));
+  const float2 a = f16x2_to_f32x2(e4m3_lo(v)), b = f16x2_to_f32x2(e4m3_hi(v));
   return f32x2_to_e4m3x2(a.x * ratio, a.y * ratio) |
          (f32x2_to_e4m3x2(b.x * ratio, b.y * ratio) << 16);
 }

@@ -63,23 +63,31 @@ int check_cache(int B, int heads_kv, int cap, int d, int r) {
 
 // Row tiles and CTAs of the attention over the cache.
 struct CaPlan {
-  int wr, row_segs, seg_rows, ctas;
+  int tile, wr, row_segs, seg_rows, ctas, stages, smem;
   size_t ml_bytes, o_bytes, score_bytes;
 };
 
 size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
-CaPlan plan_cache_attn(int B, int Hk, int R, int cap, int d, bool mass, int sms) {
+CaPlan plan_cache_attn(int B, int Hk, int R, int cap, int d, int r, bool mass, int sms) {
   CaPlan p;
-  const int tiles = (R + 15) / 16;
+  p.tile = R <= 8 ? 8 : 16;
+  const int tiles = (R + p.tile - 1) / p.tile;
   p.wr = tiles >= 3 ? 4 : tiles;
   p.row_segs = (tiles + p.wr - 1) / p.wr;
-  p.seg_rows = R < 16 * p.wr ? R : 16 * p.wr;
+  p.seg_rows = R < p.tile * p.wr ? R : p.tile * p.wr;
   // One wave of resident CTAs, fewer when that would leave warps without a block.
   const long long blocks = static_cast<long long>(B) * Hk * p.row_segs * (cap / kCacheBlock);
   const int wts = kCaWarps / p.wr;
   const long long most = (blocks + wts - 1) / wts;
-  const int wave = sms * (d == 128 ? 2 : 3);
+  // Three CTAs share an SM's 227 KB (1 KB of each is the system's), or two where
+  // three would leave a group of warps a single stage.
+  const int stage = kCacheBlock * (2 * d + r);
+  const auto fit = [&](int n) { return (227 * 1024 / n - 1024 - kCaRing) / (stage * wts); };
+  const int resident = fit(3) >= 2 ? 3 : 2;
+  const int wave = sms * resident;
+  p.stages = fit(resident) < kCaMaxStages ? fit(resident) : kCaMaxStages;
+  p.smem = kCaRing + p.stages * stage * wts;
   p.ctas = static_cast<int>(most < wave ? (most > 0 ? most : 1) : wave);
   p.ml_bytes = round256(static_cast<size_t>(p.ctas) * 2 * p.seg_rows * sizeof(float2));
   p.o_bytes = round256(static_cast<size_t>(p.ctas) * 2 * p.seg_rows * d * sizeof(float));
@@ -87,27 +95,36 @@ CaPlan plan_cache_attn(int B, int Hk, int R, int cap, int d, bool mass, int sms)
   return p;
 }
 
+constexpr int kCaMaxSmem = 227 * 1024 / 2 - 1024;
+
+template <int D, int RP, int QT, bool MASS>
+int launch_cache_attn_main(const CacheAttnArgs& a, const CaPlan& p, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  if (int rc = ensure_smem(cache_attn_kernel<D, RP, QT, MASS>, kCaMaxSmem, done)) return rc;
+  launch_pdl(cache_attn_kernel<D, RP, QT, MASS>, dim3(p.ctas), dim3(kCaThreads), p.smem, st, a);
+  return launch_status();
+}
+
 template <int D, int RP>
-int launch_cache_attn(const CacheAttnArgs& a, int ctas, cudaStream_t st) {
-  if (a.scores)
-    launch_pdl(cache_attn_kernel<D, RP, true>, dim3(ctas), dim3(kCaThreads), 0, st, a);
-  else
-    launch_pdl(cache_attn_kernel<D, RP, false>, dim3(ctas), dim3(kCaThreads), 0, st, a);
-  if (int rc = launch_status()) return rc;
-  const int rows_per = 128 / (D / 4), seg_rows = a.R < 16 * a.wr ? a.R : 16 * a.wr;
-  const dim3 grid(static_cast<unsigned>(a.B * a.Hk * a.row_segs),
-                  (seg_rows + rows_per - 1) / rows_per);
-  launch_pdl(cache_attn_combine_kernel<D>, grid, dim3(128), 0, st, a, ctas);
+int launch_cache_attn(const CacheAttnArgs& a, const CaPlan& p, cudaStream_t st) {
+  const int rc = p.tile == 8 ? a.scores ? launch_cache_attn_main<D, RP, 1, true>(a, p, st)
+                                        : launch_cache_attn_main<D, RP, 1, false>(a, p, st)
+                 : a.scores  ? launch_cache_attn_main<D, RP, 2, true>(a, p, st)
+                             : launch_cache_attn_main<D, RP, 2, false>(a, p, st);
+  if (rc != RFB_OK) return rc;
+  const dim3 grid(static_cast<unsigned>(a.B * a.Hk * a.row_segs), p.seg_rows);
+  launch_pdl(cache_attn_combine_kernel<D>, grid, dim3(128), 0, st, a,
+             static_cast<unsigned>(p.ctas));
   return launch_status();
 }
 
 template <int D>
-int dispatch_cache_attn(const CacheAttnArgs& a, int ctas, cudaStream_t st) {
+int dispatch_cache_attn(const CacheAttnArgs& a, const CaPlan& p, cudaStream_t st) {
   switch (pad_rank(a.r)) {
-    case 0: return launch_cache_attn<D, 0>(a, ctas, st);
-    case 16: return launch_cache_attn<D, 16>(a, ctas, st);
-    case 32: return launch_cache_attn<D, 32>(a, ctas, st);
-    default: return launch_cache_attn<D, 64>(a, ctas, st);
+    case 0: return launch_cache_attn<D, 0>(a, p, st);
+    case 16: return launch_cache_attn<D, 16>(a, p, st);
+    case 32: return launch_cache_attn<D, 32>(a, p, st);
+    default: return launch_cache_attn<D, 64>(a, p, st);
   }
 }
 
@@ -212,7 +229,7 @@ size_t rfb_attn_fwd_cache_workspace_size(int B, int heads, int heads_kv, int Nq,
   if (B == 0 || R == 0 || R > 0x7fffffffLL) return 0;
   DeviceInfo dev;
   if (device_info(&dev)) return 0;
-  const CaPlan p = plan_cache_attn(B, heads_kv, static_cast<int>(R), cap, d, with_mass != 0, dev.sms);
+  const CaPlan p = plan_cache_attn(B, heads_kv, static_cast<int>(R), cap, d, 0, with_mass != 0, dev.sms);
   return p.ml_bytes + p.o_bytes + p.score_bytes;
 }
 
@@ -228,7 +245,7 @@ int rfb_attn_fwd_cache(const void* q, const void* u, const void* k8, const void*
   if (B == 0 || heads == 0 || Nq == 0) return RFB_OK;
   if (heads_kv == 0 || heads % heads_kv != 0) return RFB_ERR_INVALID_ARG;
   const long long R = static_cast<long long>(heads / heads_kv) * Nq;
-  if (R > (1LL << 24) || static_cast<long long>(B) * heads_kv * ((R + 15) / 16) > 0x7fffffffLL ||
+  if (R > (1LL << 24) || static_cast<long long>(B) * heads_kv * ((R + 7) / 8) > 0x7fffffffLL / (cap / kCacheBlock + 1) ||
       (mass_out && cap > 65535 * 512))
     return RFB_ERR_UNSUPPORTED;
   if (!q || !o || !lse || !lengths || (r > 0 && !u) ||
@@ -240,8 +257,8 @@ int rfb_attn_fwd_cache(const void* q, const void* u, const void* k8, const void*
     return RFB_ERR_ALIGNMENT;
   DeviceInfo dev;
   if (int rc = device_info(&dev)) return rc;
-  const CaPlan p = plan_cache_attn(B, heads_kv, static_cast<int>(R), cap, d, mass_out != nullptr,
-                                   dev.sms);
+  const CaPlan p = plan_cache_attn(B, heads_kv, static_cast<int>(R), cap, d, r,
+                                   mass_out != nullptr, dev.sms);
   if (!workspace || workspace_bytes < p.ml_bytes + p.o_bytes + p.score_bytes)
     return RFB_ERR_WORKSPACE;
   if (!aligned16(workspace)) return RFB_ERR_ALIGNMENT;
@@ -260,13 +277,17 @@ int rfb_attn_fwd_cache(const void* q, const void* u, const void* k8, const void*
   a.part_o = reinterpret_cast<float*>(ws + p.ml_bytes);
   a.scores = mass_out ? reinterpret_cast<float*>(ws + p.ml_bytes + p.o_bytes) : nullptr;
   a.B = B, a.Hk = heads_kv, a.R = static_cast<int>(R), a.Nq = Nq, a.cap = cap, a.r = r;
-  a.wr = p.wr, a.row_segs = p.row_segs;
+  a.tile = p.tile, a.wr = p.wr, a.row_segs = p.row_segs;
   a.causal = causal;
+  a.stages = p.stages;
+  a.err_word = dev.err_word;
+  a.wait_ns = g_wait_limit_ns.load();
+  a.fail_site = g_fail_site.load();
   a.scale_log2 = scale * kLog2e;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  int rc = d == 32   ? dispatch_cache_attn<32>(a, p.ctas, st)
-           : d == 64 ? dispatch_cache_attn<64>(a, p.ctas, st)
-                     : dispatch_cache_attn<128>(a, p.ctas, st);
+  int rc = d == 32   ? dispatch_cache_attn<32>(a, p, st)
+           : d == 64 ? dispatch_cache_attn<64>(a, p, st)
+                     : dispatch_cache_attn<128>(a, p, st);
   if (rc != RFB_OK || !mass_out || cap == 0) return rc;
   const dim3 grid(static_cast<unsigned>(B) * heads_kv, (cap + 511) / 512);
   launch_pdl(cache_mass_kernel, grid, dim3(128), 0, st, a, mass, mass_out, decay);
