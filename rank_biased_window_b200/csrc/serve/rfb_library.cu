@@ -14,6 +14,22 @@ namespace {
 
 bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+// device_info() with the answer kept per thread: the short calls of a decode
+// step come thousands of times a second from the same thread and device.
+int current_device(DeviceInfo* out) {
+  static thread_local DeviceInfo known;
+  static thread_local int known_dev = -1;
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, kSiteGetDevice);
+  if (dev != known_dev) {
+    if (int rc = device_info(&known)) return rc;
+    known_dev = dev;
+  }
+  *out = known;
+  return RFB_OK;
+}
+
 // ------------------------------------------------------------------ rotary
 template <typename T, bool HALF, bool VEC>
 int launch_rotary(RotArgs& a, int B, int sms, cudaStream_t st) {
@@ -154,7 +170,7 @@ int rfb_rotary(const void* q, const void* k, void* q_out, void* k_out, const int
       !aligned_to(k_out, elem) || !aligned_to(positions, 4) || !aligned_to(freqs, 8))
     return RFB_ERR_ALIGNMENT;
   DeviceInfo dev;
-  if (int rc = device_info(&dev)) return rc;
+  if (int rc = current_device(&dev)) return rc;
   RotArgs a = {};
   a.x[0] = q, a.x[1] = k;
   a.y[0] = q_out, a.y[1] = k_out;
@@ -209,7 +225,7 @@ int rfb_cache_append(const void* k, const void* v, const void* w, const long lon
   a.blocks = static_cast<int>((static_cast<long long>(n) + kCacheBlock - 2) / kCacheBlock) + 1;
   if (a.blocks > cap / kCacheBlock) a.blocks = cap / kCacheBlock;
   DeviceInfo dev;
-  if (int rc = device_info(&dev)) return rc;
+  if (int rc = current_device(&dev)) return rc;
   const long long units = static_cast<long long>(a.blocks) * a.tensors;
   const dim3 grid(static_cast<unsigned>((units + kAppendWarps - 1) / kAppendWarps), heads_kv, B);
   const dim3 block(kAppendWarps * 32);
@@ -228,7 +244,7 @@ size_t rfb_attn_fwd_cache_workspace_size(int B, int heads, int heads_kv, int Nq,
   const long long R = static_cast<long long>(heads / heads_kv) * Nq;
   if (B == 0 || R == 0 || R > 0x7fffffffLL) return 0;
   DeviceInfo dev;
-  if (device_info(&dev)) return 0;
+  if (current_device(&dev)) return 0;
   const CaPlan p = plan_cache_attn(B, heads_kv, static_cast<int>(R), cap, d, 0, with_mass != 0, dev.sms);
   return p.ml_bytes + p.o_bytes + p.score_bytes;
 }
@@ -256,7 +272,7 @@ int rfb_attn_fwd_cache(const void* q, const void* u, const void* k8, const void*
       !aligned16(w_scale) || !aligned16(mass) || !aligned16(mass_out) || !aligned_to(lengths, 4))
     return RFB_ERR_ALIGNMENT;
   DeviceInfo dev;
-  if (int rc = device_info(&dev)) return rc;
+  if (int rc = current_device(&dev)) return rc;
   const CaPlan p = plan_cache_attn(B, heads_kv, static_cast<int>(R), cap, d, r,
                                    mass_out != nullptr, dev.sms);
   if (!workspace || workspace_bytes < p.ml_bytes + p.o_bytes + p.score_bytes)
@@ -339,7 +355,7 @@ int rfb_cache_evict(const void* k8, const void* v8, const void* w8, const float*
   a.Hk = heads_kv, a.cap = cap, a.to_cap = cap_out, a.d = d, a.r = r;
   a.keep = keep, a.recent = recent;
   DeviceInfo dev;
-  if (int rc = device_info(&dev)) return rc;
+  if (int rc = current_device(&dev)) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int bh = B * heads_kv;
   launch_pdl(cache_select_kernel, dim3(bh), dim3(kSelThreads), 0, st, a);

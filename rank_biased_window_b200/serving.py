@@ -46,29 +46,27 @@ def _cuda(name, t):
     return t.device
 
 
-class _launch_on:
-    """The device and stream of a call: makes both current, so that what the
-    call allocates belongs to the stream it runs on."""
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
-    def __init__(self, device, stream):
-        self.device = _on_device(device)
-        self.stream = None if stream is None else torch.cuda.stream(stream)
-        self.torch_device = device
 
-    def __enter__(self):
-        self.device.__enter__()
-        if self.stream is not None:
-            self.stream.__enter__()
-        return torch.cuda.current_stream(self.torch_device).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.stream is not None:
-            self.stream.__exit__(*exc)
-        self.device.__exit__(*exc)
+def _launch(device, stream, call, *args):
+    """call(*args, stream pointer) with the device and the stream current, so
+    that what the call allocates belongs to the stream it runs on.  The usual
+    case, the current stream of the current device, changes neither."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return call(*args, _raw_stream(device.index))
+    with _on_device(device):
+        if stream is None:
+            return call(*args, _raw_stream(device.index))
+        with torch.cuda.stream(stream):
+            return call(*args, stream.cuda_stream)
 
 
 def _p(t):
     return None if t is None else t.data_ptr()
+
+
+_Strides6, _Strides9 = ctypes.c_longlong * 6, ctypes.c_longlong * 9
 
 
 # ------------------------------------------------------------------- rotary
@@ -117,53 +115,52 @@ def rotary_frequencies(rot, base=10000.0, *, scaling="none", factor=1.0, origina
     return freqs.to(device) if device is not None else freqs, amplitude
 
 
-def _rotary(q, k, positions, freqs, layout, amplitude, inverse, q_out, k_out, stream):
-    dev = _cuda("q", q)
+def _rotary(q, k, positions, freqs, layout, amplitude, inverse, q_out, k_out, st):
+    dev, dtype, shape = q.device, q.dtype, q.shape
     if layout not in _LAYOUTS:
         raise ValueError("layout must be 'half' or 'interleaved'")
-    dt = _DTYPES.get(q.dtype)
-    if dt is None:
-        raise TypeError(f"q must be bfloat16, float16 or float32, got {q.dtype}")
-    if q.dim() != 4:
+    if dtype not in _DTYPES:
+        raise TypeError(f"q must be bfloat16, float16 or float32, got {dtype}")
+    if len(shape) != 4:
         raise ValueError("q must be [B, H, N, d]")
-    B, H, N, d = q.shape
-    Hk = 0
+    B, H, N, d = shape
+    sq, Hk, sk = q.stride(), 0, (0, 0, 0, 1)
     if k is not None:
         if not isinstance(k, torch.Tensor) or k.dim() != 4:
             raise ValueError("k must be [B, H, N, d]")
-        Hk = k.shape[1]
-        _require("k", k, q.dtype, (B, Hk, N, d), dev, contiguous=False)
-    for name, t in (("q", q), ("k", k)):
-        if t is not None and d > 1 and t.stride(3) != 1:
-            raise ValueError(f"{name} must have contiguous channels")
+        Hk, sk = k.shape[1], k.stride()
+        _require("k", k, dtype, (B, Hk, N, d), dev, False)
+    if d > 1 and (sq[3] != 1 or sk[3] != 1):
+        raise ValueError(f"{'q' if sq[3] != 1 else 'k'} must have contiguous channels")
     if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1:
         raise ValueError("freqs must be [rot / 2]")
-    rot = 2 * freqs.shape[0]
-    _require("freqs", freqs, torch.float64, (rot // 2,), dev)
-    if rot > d:
-        raise ValueError(f"freqs has {rot // 2} pairs, more than half of d = {d}")
+    pairs = freqs.shape[0]
+    _require("freqs", freqs, torch.float64, (pairs,), dev)
+    if 2 * pairs > d:
+        raise ValueError(f"freqs has {pairs} pairs, more than half of d = {d}")
     if not isinstance(positions, torch.Tensor) or positions.dim() not in (1, 2):
         raise ValueError("positions must be [N] or [B, N]")
-    _require("positions", positions, torch.int32, (N,) if positions.dim() == 1 else (B, N), dev)
-    with _launch_on(dev, stream) as st:
-        outs = []
-        for name, t, o in (("q_out", q, q_out), ("k_out", k, k_out)):
-            if t is None:
-                outs.append(None)
-                continue
-            if o is None:
-                o = torch.empty(t.shape, dtype=t.dtype, device=dev)
-            else:
-                _require(name, o, t.dtype, t.shape, dev)
-            outs.append(o)
-        qs = (ctypes.c_longlong * 3)(*q.stride()[:3])
-        ks = None if k is None else (ctypes.c_longlong * 3)(*k.stride()[:3])
-        rc = load_library().rfb_rotary(
-            q.data_ptr(), _p(k), outs[0].data_ptr(), _p(outs[1]), positions.data_ptr(),
-            freqs.data_ptr(), B, H, Hk, N, d, rot, qs, ks,
-            N if positions.dim() == 2 else 0, _LAYOUTS[layout], dt, amplitude, inverse, st)
-    _check(rc, "rfb_rotary")
-    return outs[0], outs[1]
+    own_rows = positions.dim() == 2
+    _require("positions", positions, torch.int32, (B, N) if own_rows else (N,), dev)
+    if q_out is None:
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    else:
+        _require("q_out", q_out, dtype, shape, dev)
+    if k is None:
+        k_out = None
+    elif k_out is None:
+        k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+    else:
+        _require("k_out", k_out, dtype, k.shape, dev)
+    strides = _Strides6(sq[0], sq[1], sq[2], sk[0], sk[1], sk[2])
+    at = ctypes.addressof(strides)
+    rc = load_library().rfb_rotary(
+        q.data_ptr(), _p(k), q_out.data_ptr(), _p(k_out), positions.data_ptr(), freqs.data_ptr(),
+        B, H, Hk, N, d, 2 * pairs, at, at + 24, N if own_rows else 0, _LAYOUTS[layout],
+        _DTYPES[dtype], amplitude, inverse, st)
+    if rc:
+        _check(rc, "rfb_rotary")
+    return q_out, k_out
 
 
 def rotary_fwd(q, k, positions, freqs, *, layout="half", amplitude=1.0, q_out=None, k_out=None,
@@ -176,13 +173,15 @@ def rotary_fwd(q, k, positions, freqs, *, layout="half", amplitude=1.0, q_out=No
     layout that attention takes.  positions: int32 [N] or [B, N]; freqs: fp64
     [rot / 2] from rotary_frequencies (channels from rot on pass through).
     """
-    return _rotary(q, k, positions, freqs, layout, amplitude, 0, q_out, k_out, stream)
+    return _launch(_cuda("q", q), stream, _rotary, q, k, positions, freqs, layout, amplitude, 0,
+                   q_out, k_out)
 
 
 def rotary_bwd(dq, dk, positions, freqs, *, layout="half", amplitude=1.0, q_out=None, k_out=None,
                stream=None):
     """Gradients of q and k from those of rotary_fwd's outputs (the inverse turn)."""
-    return _rotary(dq, dk, positions, freqs, layout, amplitude, 1, q_out, k_out, stream)
+    return _launch(_cuda("dq", dq), stream, _rotary, dq, dk, positions, freqs, layout, amplitude, 1,
+                   q_out, k_out)
 
 
 class RFBRotary(torch.autograd.Function):
@@ -223,7 +222,7 @@ class Cache8:
     """
 
     __slots__ = ("k", "v", "w", "k_scale", "v_scale", "w_scale", "mass", "device", "B", "Hk", "cap",
-                 "d", "r", "_ptrs")
+                 "d", "r", "_ptrs", "_workspace_bytes")
 
     def __init__(self, k, v, w, k_scale, v_scale, w_scale, mass=None):
         dev = _cuda("k", k)
@@ -252,6 +251,7 @@ class Cache8:
         self.mass, self.device = mass, dev
         self.B, self.Hk, self.cap, self.d, self.r = B, Hk, cap, d, r
         self._ptrs = tuple(_p(t) for t in (k, v, w, k_scale, v_scale, w_scale))
+        self._workspace_bytes = {}  # by (heads, Nq, with mass)
 
     @classmethod
     def create(cls, B, heads_kv, capacity, d, r=0, *, mass=False, device="cuda"):
@@ -276,10 +276,6 @@ class Cache8:
         return codes.float() * scales.repeat_interleave(CACHE_BLOCK, dim=2)[..., None]
 
 
-def _ints(name, t, B, device):
-    _require(name, t, torch.int32, (B,), device)
-
-
 def cache_append(cache, k, v, w=None, *, start, counts=None, stream=None):
     """Writes rows k, v [B, Hk, n, d] and w [B, Hk, n, r] (bf16) into the cache
     at positions start[b] .. start[b] + counts[b] - 1 (counts None: all n).
@@ -290,31 +286,34 @@ def cache_append(cache, k, v, w=None, *, start, counts=None, stream=None):
     """
     if not isinstance(cache, Cache8):
         raise TypeError("cache must be a Cache8")
+    return _launch(cache.device, stream, _append, cache, k, v, w, start, counts)
+
+
+def _append(cache, k, v, w, start, counts, st):
     dev, B, Hk, d, r = cache.device, cache.B, cache.Hk, cache.d, cache.r
     if not isinstance(k, torch.Tensor) or k.dim() != 4:
         raise ValueError("k must be [B, Hk, n, d]")
     n = k.shape[2]
-    _require("k", k, torch.bfloat16, (B, Hk, n, d), dev, contiguous=False)
-    _require("v", v, torch.bfloat16, (B, Hk, n, d), dev, contiguous=False)
+    _require("k", k, torch.bfloat16, (B, Hk, n, d), dev, False)
+    _require("v", v, torch.bfloat16, (B, Hk, n, d), dev, False)
     if r:
-        _require("w", w, torch.bfloat16, (B, Hk, n, r), dev, contiguous=False)
+        _require("w", w, torch.bfloat16, (B, Hk, n, r), dev, False)
     elif w is not None:
         raise ValueError("w given, but the cache holds no factors (r = 0)")
-    _ints("start", start, B, dev)
+    _require("start", start, torch.int32, (B,), dev)
     if counts is not None:
-        _ints("counts", counts, B, dev)
-    if n == 0:
-        return cache
+        _require("counts", counts, torch.int32, (B,), dev)
     sk, sv, sw = k.stride(), v.stride(), w.stride() if r else (0, 0, 0, 1)
-    for name, s in (("k", sk), ("v", sv), ("w", sw)):
-        if s[3] != 1 or (s[0] | s[1] | s[2]) % 8:
-            raise ValueError(f"{name} must have contiguous channels and strides of multiples of 8")
-    strides = (ctypes.c_longlong * 9)(*sk[:3], *sv[:3], *sw[:3])
-    with _launch_on(dev, stream) as st:
-        rc = load_library().rfb_cache_append(
-            k.data_ptr(), v.data_ptr(), _p(w), strides, *cache._ptrs, _p(cache.mass),
-            start.data_ptr(), _p(counts), B, Hk, n, cache.cap, d, r, st)
-    _check(rc, "rfb_cache_append")
+    if sk[3] * sv[3] * sw[3] != 1 or (sk[0] | sk[1] | sk[2] | sv[0] | sv[1] | sv[2] | sw[0] | sw[1]
+                                      | sw[2]) % 8:
+        if n:
+            raise ValueError("k, v and w must have contiguous channels and strides of multiples of 8")
+    strides = _Strides9(sk[0], sk[1], sk[2], sv[0], sv[1], sv[2], sw[0], sw[1], sw[2])
+    rc = load_library().rfb_cache_append(
+        k.data_ptr(), v.data_ptr(), _p(w), ctypes.addressof(strides), *cache._ptrs, _p(cache.mass),
+        start.data_ptr(), _p(counts), B, Hk, n, cache.cap, d, r, st)
+    if rc:
+        _check(rc, "rfb_cache_append")
     return cache
 
 
@@ -340,10 +339,15 @@ def attn_fwd_cache(q, u, cache, lengths, scale=None, *, causal=True, mass=None, 
     """
     if not isinstance(cache, Cache8):
         raise TypeError("cache must be a Cache8")
+    return _launch(cache.device, stream, _attn, q, u, cache, lengths, scale, causal, mass, mass_out,
+                   decay, out, lse, workspace)
+
+
+def _attn(q, u, cache, lengths, scale, causal, mass, mass_out, decay, out, lse, workspace, st):
     dev, B, Hk, cap, d, r = cache.device, cache.B, cache.Hk, cache.cap, cache.d, cache.r
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError("q must be [B, H, Nq, d]")
-    H, Nq = q.shape[1], q.shape[2]
+    _, H, Nq, _ = q.shape
     _require("q", q, torch.bfloat16, (B, H, Nq, d), dev)
     if r:
         _require("u", u, torch.bfloat16, (B, H, Nq, r), dev)
@@ -351,41 +355,41 @@ def attn_fwd_cache(q, u, cache, lengths, scale=None, *, causal=True, mass=None, 
         raise ValueError("u given, but the cache holds no factors (r = 0)")
     if H and (Hk == 0 or H % Hk):
         raise ValueError(f"{H} query heads are not a multiple of the cache's {Hk}")
-    _ints("lengths", lengths, B, dev)
+    _require("lengths", lengths, torch.int32, (B,), dev)
     if mass is not None:
         if mass_out is None:
             raise ValueError("mass needs mass_out (which may be the same tensor)")
         _require("mass", mass, torch.float32, (B, Hk, cap), dev)
     if mass_out is not None:
         _require("mass_out", mass_out, torch.float32, (B, Hk, cap), dev)
-    s = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    lib = load_library()
-    with _launch_on(dev, stream) as st:
-        if out is None:
-            out = torch.empty((B, H, Nq, d), dtype=torch.bfloat16, device=dev)
-        else:
-            _require("out", out, torch.bfloat16, (B, H, Nq, d), dev)
-        if lse is None:
-            lse = torch.empty((B, H, Nq), dtype=torch.float32, device=dev)
-        else:
-            _require("lse", lse, torch.float32, (B, H, Nq), dev)
-        if workspace is None:
-            need = lib.rfb_attn_fwd_cache_workspace_size(B, H, Hk, Nq, cap, d,
-                                                         0 if mass_out is None else 1)
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-        elif (not isinstance(workspace, torch.Tensor) or workspace.device != dev
-              or not workspace.is_contiguous()):
-            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-        rc = lib.rfb_attn_fwd_cache(
-            q.data_ptr(), _p(u), *cache._ptrs, lengths.data_ptr(), _p(mass), _p(mass_out),
-            float(decay), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), B, H, Hk, Nq, cap, d, r, s,
-            1 if causal else 0, st)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _require("out", out, torch.bfloat16, (B, H, Nq, d), dev)
+    if lse is None:
+        lse = cache.k_scale.new_empty((B, H, Nq))
+    else:
+        _require("lse", lse, torch.float32, (B, H, Nq), dev)
+    if workspace is None:
+        key = (H, Nq, mass_out is not None)
+        need = cache._workspace_bytes.get(key)
+        if need is None:
+            need = cache._workspace_bytes[key] = attn_cache_workspace_size(cache, *key)
+        workspace = cache.k_scale.new_empty((need + 19) // 4)
+    elif (not isinstance(workspace, torch.Tensor) or workspace.device != dev
+          or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    rc = load_library().rfb_attn_fwd_cache(
+        q.data_ptr(), _p(u), *cache._ptrs, lengths.data_ptr(), _p(mass), _p(mass_out), decay,
+        out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), B, H, Hk, Nq, cap, d, r,
+        d ** -0.5 if scale is None else scale, 1 if causal else 0, st)
     if rc == RFB_ERR_WORKSPACE:
         raise RuntimeError(
             f"rfb_attn_fwd_cache: workspace of "
             f"{attn_cache_workspace_size(cache, H, Nq, mass_out is not None)} bytes needed")
-    _check(rc, "rfb_attn_fwd_cache")
+    if rc:
+        _check(rc, "rfb_attn_fwd_cache")
     return out, lse
 
 
@@ -414,13 +418,17 @@ def cache_evict(cache, lengths, keep, recent=0, *, out=None, stream=None):
         raise ValueError(f"keep must be in [1, {to.cap}], the receiving capacity")
     if recent < 0:
         raise ValueError("recent must be >= 0")
-    _ints("lengths", lengths, B, dev)
-    with _launch_on(dev, stream) as st:
-        new_lengths = torch.empty((B,), dtype=torch.int32, device=dev)
-        kept = torch.empty((B, Hk, keep), dtype=torch.int32, device=dev)
-        rc = load_library().rfb_cache_evict(
-            *cache._ptrs, cache.mass.data_ptr(), *to._ptrs, to.mass.data_ptr(), lengths.data_ptr(),
-            new_lengths.data_ptr(), kept.data_ptr(), B, Hk, cache.cap, to.cap, cache.d, cache.r,
-            keep, min(recent, keep), st)
-    _check(rc, "rfb_cache_evict")
+    _require("lengths", lengths, torch.int32, (B,), dev)
+    return _launch(dev, stream, _evict, cache, to, lengths, keep, min(recent, keep))
+
+
+def _evict(cache, to, lengths, keep, recent, st):
+    new_lengths = torch.empty_like(lengths)
+    kept = lengths.new_empty((cache.B, cache.Hk, keep))
+    rc = load_library().rfb_cache_evict(
+        *cache._ptrs, cache.mass.data_ptr(), *to._ptrs, to.mass.data_ptr(), lengths.data_ptr(),
+        new_lengths.data_ptr(), kept.data_ptr(), cache.B, cache.Hk, cache.cap, to.cap, cache.d,
+        cache.r, keep, recent, st)
+    if rc:
+        _check(rc, "rfb_cache_evict")
     return new_lengths, kept
