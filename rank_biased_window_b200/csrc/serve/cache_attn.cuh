@@ -10,8 +10,9 @@
 // lane loads whole 8- or 16-byte pieces of rows and the queries are permuted to
 // match), become fp16 there (exact) and enter m16n8k16 MMAs with fp32
 // accumulators.  Softmax statistics and sums are fp32; the probabilities are
-// rounded to fp16 for the product with V (2^-12 relative, below the bf16
-// rounding of O).  Queries enter as fp16 scaled by a power of two per row,
+// rounded to fp16 for the product with V (2^-11 relative, below the bf16
+// rounding of O), lifted by 2^15 so that this holds down to 2^-29 of the largest:
+// a token of small weight may have a large value.  Queries enter as fp16 scaled by a power of two per row,
 // which holds every bf16 within 2^-29 of the row's largest exactly.
 //
 // Bound by HBM: 2 d + r bytes a token and head.  With at most 16 rows in a
@@ -21,7 +22,8 @@
 //
 // Work split: the blocks of all (sequence, key head, row tile) segments form one
 // line, cut into equal parts, one per CTA, so ragged lengths and few long
-// sequences fill the chip alike.  A segment that one CTA holds whole is finished
+// sequences fill the chip alike; a segment counts kCaSegmentCost blocks more than
+// it has, since beginning one and joining its warps takes that long.  A segment that one CTA holds whole is finished
 // there; others leave (max, sum, O) partials, which cache_attn_combine_kernel
 // joins in order (results do not depend on timing).
 #pragma once
@@ -32,6 +34,8 @@ namespace rfb {
 
 constexpr int kCaWarps = 4;
 constexpr int kCaThreads = kCaWarps * 32;
+constexpr unsigned kCaSegmentCost = 4;
+constexpr float kCaLift = 15.f;  // weights are held as 2^(x - max + 15)
 
 struct CacheAttnArgs {
   const __nv_bfloat16* q;  // [B, Hk, R, d], R = group * Nq
@@ -42,6 +46,9 @@ struct CacheAttnArgs {
   __nv_bfloat16* o;
   float* lse;
   float* scores;  // [B, Hk, R, cap] log2 scores for the mass, or null
+  const float* mass;
+  float* mass_out;
+  float decay;
   float* part_o;  // [ctas][2][rows of a segment][d]
   float2* part_ml;
   int B, Hk, R, Nq, cap, r;
@@ -59,20 +66,24 @@ struct CacheAttnArgs {
 __device__ __forceinline__ int cache_blocks(const CacheAttnArgs& a, int b) {
   return (min(max(a.lengths[b], 0), a.cap) + kCacheBlock - 1) / kCacheBlock;
 }
+// Length on the line of a segment of n blocks: its cost, then its blocks; an
+// empty one has none.
+__device__ __forceinline__ unsigned line_length(int n) { return n > 0 ? n + kCaSegmentCost : 0u; }
 
-// Blocks of all sequences, and of those before sequence b (all lanes call it).
-__device__ __forceinline__ void count_blocks(const CacheAttnArgs& a, int b, unsigned& before,
+// Line length of all sequences (one segment each), and of those before sequence b
+// (all lanes call it).
+__device__ __forceinline__ void count_line(const CacheAttnArgs& a, int b, unsigned& before,
                                              unsigned& total) {
   before = total = 0;
   for (int b0 = 0; b0 < a.B; b0 += 32) {
     const int x = b0 + static_cast<int>(lane_id());
-    const unsigned n = x < a.B ? cache_blocks(a, x) : 0;
+    const unsigned n = x < a.B ? line_length(cache_blocks(a, x)) : 0;
     total += __reduce_add_sync(0xffffffffu, n);
     before += __reduce_add_sync(0xffffffffu, x < b ? n : 0u);
   }
 }
 
-// The line of W blocks cut over n CTAs: the first W % n hold W / n + 1, the rest W / n.
+// A line of length W cut over n CTAs: the first W % n hold W / n + 1, the rest W / n.
 struct Cut {
   unsigned base, extra;
   __device__ __forceinline__ Cut(unsigned W, unsigned n) : base(W / n), extra(W - W / n * n) {}
@@ -84,17 +95,18 @@ struct Cut {
 };
 
 // The CTA's part [at, stop) of the line and where it starts: sequence b, whose
-// segments have nb blocks each; segment seg of it, block blk.
+// segments have nb blocks each; segment seg of it, `in` from that segment's start.
 struct Place {
   unsigned at, stop;
-  int b, nb, seg, blk;
+  int b, nb, seg;
+  unsigned in;
 };
 __device__ __forceinline__ Place place_of(const CacheAttnArgs& a, unsigned mult) {
   Place p = {};
   const int lane = lane_id();
   unsigned total = 0, n = 0, incl = 0;
   for (int b0 = 0; b0 < a.B; b0 += 32) {  // at most 32 sequences: one round, kept below
-    n = b0 + lane < a.B ? cache_blocks(a, b0 + lane) : 0;
+    n = b0 + lane < a.B ? line_length(cache_blocks(a, b0 + lane)) : 0;
     incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -111,7 +123,7 @@ __device__ __forceinline__ Place place_of(const CacheAttnArgs& a, unsigned mult)
   unsigned before = 0;
   for (int b0 = 0;; b0 += 32) {
     if (a.B > 32) {
-      n = b0 + lane < a.B ? cache_blocks(a, b0 + lane) : 0;
+      n = b0 + lane < a.B ? line_length(cache_blocks(a, b0 + lane)) : 0;
       incl = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -129,9 +141,10 @@ __device__ __forceinline__ Place place_of(const CacheAttnArgs& a, unsigned mult)
     }
     before += __shfl_sync(0xffffffffu, incl, 31);
   }
-  const unsigned in_seq = p.at - before * mult;
-  p.seg = in_seq / p.nb;
-  p.blk = in_seq - p.seg * p.nb;
+  const unsigned in_seq = p.at - before * mult, len = p.nb;
+  p.seg = in_seq / len;
+  p.in = in_seq - p.seg * len;
+  p.nb = len - kCaSegmentCost;
   return p;
 }
 
@@ -387,12 +400,11 @@ __global__ void __launch_bounds__(kCaThreads, 3)
   const uint32_t w_bytes = RP > 0 ? kCacheBlock * a.r : 0, stage_bytes = w_off + w_bytes;
   const uint32_t ring = smem_u32(smem) + kCaRing + wt * stages * stage_bytes;
   const uint32_t full = smem_u32(&head.full[wt][0]), empty = smem_u32(&head.empty[wt][0]);
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < kCaWarps * kCaMaxStages; ++i) {
-      mbar_init(smem_u32(&head.full[0][0]) + 8 * i, 1);
-      mbar_init(smem_u32(&head.empty[0][0]) + 8 * i, a.wr);
-    }
-    head.abort_flag = head.drain_flag = 0;
+  if (warp == 0) {
+    static_assert(kCaWarps * kCaMaxStages == 32, "one lane a pair of barriers");
+    mbar_init(smem_u32(&head.full[0][0]) + 8 * lane, 1);
+    mbar_init(smem_u32(&head.empty[0][0]) + 8 * lane, a.wr);
+    if (lane == 0) head.abort_flag = head.drain_flag = 0;
     fence_mbar_init();
   }
   __syncthreads();
@@ -404,8 +416,13 @@ __global__ void __launch_bounds__(kCaThreads, 3)
   unsigned at = place.at;
   const unsigned stop = place.stop;
   if (at >= stop) return;
-  int b = place.b, nb = place.nb, seg = place.seg, blk0 = place.blk;
-  int blk1 = static_cast<int>(min(static_cast<unsigned>(nb), blk0 + (stop - at)));
+  int b = place.b, nb = place.nb, seg = place.seg;
+  // this CTA's blocks [blk0, blk1) of the segment; none where its part ends within the cost
+  const auto first_block = [](unsigned in) {
+    return static_cast<int>(max(in, kCaSegmentCost) - kCaSegmentCost);
+  };
+  unsigned in = place.in;
+  int blk0 = first_block(in), blk1 = min(nb, first_block(in + (stop - at)));
   const int seg_rows = min(a.R, QR * a.wr);
   bool first = true, dead = false;
   const bool leader = wr == 0;
@@ -420,7 +437,7 @@ __global__ void __launch_bounds__(kCaThreads, 3)
     const long long bh = static_cast<long long>(b) * a.Hk + h;
     const int row0 = (rs * a.wr + wr) * QR;
     // the segment after this one
-    const unsigned next_at = at + (blk1 - blk0);
+    const unsigned next_at = at + (nb + kCaSegmentCost - in);
     int nseg = seg + 1, nxb = b, nnb = nb;
     if (nseg == mult) {
       nseg = 0;
@@ -429,10 +446,9 @@ __global__ void __launch_bounds__(kCaThreads, 3)
       } while (nxb < a.B && cache_blocks(a, nxb) == 0);
       if (nxb < a.B) nnb = cache_blocks(a, nxb);
     }
-    const int nblk1 =
-        next_at < stop ? static_cast<int>(min(static_cast<unsigned>(nnb), stop - next_at)) : 0;
-    const int mine = (blk1 - blk0 - wt + wts - 1) / wts;           // this group's blocks here
-    const int ahead = mine + (nblk1 - wt + wts - 1) / wts;         // and with the next segment's
+    const int nblk1 = next_at < stop ? min(nnb, first_block(stop - next_at)) : 0;
+    const int mine = max(blk1 - blk0 - wt + wts - 1, 0) / wts;      // this group's blocks here
+    const int ahead = mine + max(nblk1 - wt + wts - 1, 0) / wts;    // and with the next segment's
     const long long nbh = static_cast<long long>(nxb) * a.Hk + nseg / a.row_segs;
 
     // Loads blocks until `upto` of them (counted from this segment's first) are under way.
@@ -461,6 +477,7 @@ __global__ void __launch_bounds__(kCaThreads, 3)
       }
     };
     pump(stages);
+    if (blk0 == blk1) break;  // only at the end of the part
 
     // Queries as B fragments (lane g: query g of each tile); scores, sums and O are
     // held for queries 2 t, 2 t + 1.
@@ -649,8 +666,8 @@ __global__ void __launch_bounds__(kCaThreads, 3)
       uint32_t p[2][QT][2];
 #pragma unroll
       for (int q = 0; q < QT; ++q) {
-        const float base[2] = {m[q][0] == -INFINITY ? 0.f : m[q][0],
-                               m[q][1] == -INFINITY ? 0.f : m[q][1]};
+        const float base[2] = {m[q][0] == -INFINITY ? 0.f : m[q][0] - kCaLift,
+                               m[q][1] == -INFINITY ? 0.f : m[q][1] - kCaLift};
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
 #pragma unroll
@@ -698,6 +715,9 @@ __global__ void __launch_bounds__(kCaThreads, 3)
 #pragma unroll
         for (int k = 0; k < 4; ++k) oacc[n][q][k] *= unit;
     }
+    // from here on m is what the sums are relative to
+#pragma unroll
+    for (int q = 0; q < QT; ++q) m[q][0] -= kCaLift, m[q][1] -= kCaLift;
     const bool whole = blk0 == 0 && blk1 == nb;
     const int slot = first ? 0 : 1;
     if (wts > 1) {
@@ -808,6 +828,7 @@ __global__ void __launch_bounds__(kCaThreads, 3)
     first = false;
     at = next_at;
     b = nxb, seg = nseg, nb = nnb;
+    in = 0;
     blk0 = 0;
     blk1 = nblk1;
   }
@@ -819,10 +840,116 @@ __global__ void __launch_bounds__(kCaThreads, 3)
   }
 }
 
+// Where the partials of segment (b, seg) lie: CTAs i0 .. i1 hold blocks of it, each
+// as its first segment (slot 0), but for one that began in an earlier one.
+struct Parts {
+  unsigned i0, n;  // n == 0: no token; 1: the CTA finished the segment itself
+  unsigned late;
+  __device__ __forceinline__ long long index(unsigned k, int seg_rows, int rr) const {
+    return (static_cast<long long>(i0 + k) * 2 + (k == 0 ? late : 0u)) * seg_rows + rr;
+  }
+};
+__device__ __forceinline__ Parts parts_of(const CacheAttnArgs& a, int b, int seg, unsigned ctas) {
+  const int mult = a.Hk * a.row_segs;
+  unsigned before, total;
+  count_line(a, b, before, total);
+  const unsigned len = line_length(cache_blocks(a, b));
+  if (len == 0) return Parts{0, 0, 0};
+  const unsigned s0 = before * mult + seg * len;
+  const Cut cut(total * mult, ctas);
+  const unsigned i0 = cut.holder(s0 + kCaSegmentCost), i1 = cut.holder(s0 + len - 1);
+  return Parts{i0, i1 - i0 + 1, cut.start(i0) < s0 ? 1u : 0u};
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Warps of a mass CTA that share tokens, each with every mass_row_warps-th row.
+__host__ __device__ __forceinline__ int mass_row_warps(int R) { return R >= 4 ? 4 : R >= 2 ? 2 : 1; }
+__host__ __device__ __forceinline__ int mass_tokens(int R) { return 512 / mass_row_warps(R); }
+
+// mass_out = decay mass + sum over the key head's rows of exp(x - LSE) for
+// mass_tokens of key head bh, 4 a thread.  LSE is joined here again from the
+// partials, so that this needs no kernel behind the join of O.
+__device__ __forceinline__ void add_mass(const CacheAttnArgs& a, unsigned ctas, int bh, int chunk) {
+  __shared__ float lse2[128];  // of 128 rows, in log2 units
+  __shared__ float4 part[3][32];
+  const int b = bh / a.Hk, h = bh - b * a.Hk, seg_tile = a.wr * a.tile;
+  const int rw = mass_row_warps(a.R), warp = warp_id(), lane = lane_id();
+  const int t0 = chunk * mass_tokens(a.R) + (warp / rw) * 128 + lane * 4;
+  const int L = min(a.lengths[b], a.cap);
+  if (chunk * mass_tokens(a.R) >= L) return;
+  const int seg_rows = min(a.R, a.tile * a.wr);
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float* s = a.scores + static_cast<long long>(bh) * a.R * a.cap + t0;
+  for (int r0 = 0; r0 < a.R; r0 += 128) {
+    const int rows = min(128, a.R - r0);
+    // lanes that share a row: 32 for up to 4 rows, 1 for 128
+    int per = 32;
+    while (per * rows > 128) per >>= 1;
+    const int i = threadIdx.x / per, row = r0 + i, rs = row / seg_tile;
+    float m = -INFINITY, l = 0.f;
+    bool own = false;
+    for (int r = r0 / seg_tile; r <= (r0 + rows - 1) / seg_tile; ++r) {
+      const Parts parts = parts_of(a, b, h * a.row_segs + r, ctas);
+      if (i >= rows || rs != r) continue;
+      own = parts.n == 1;
+      if (own) continue;
+#pragma unroll 4
+      for (unsigned k = threadIdx.x % per; k < parts.n; k += per) {
+        const float2 ml = a.part_ml[parts.index(k, seg_rows, row - rs * seg_tile)];
+        const float mn = fmaxf(m, ml.x), base = mn == -INFINITY ? 0.f : mn;
+        l = l * fast_exp2(m - base) + ml.y * fast_exp2(ml.x - base);
+        m = mn;
+      }
+    }
+    float top = m;
+    for (int o = per >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    l *= fast_exp2(m - (top == -INFINITY ? 0.f : top));
+    for (int o = per >> 1; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (i < rows && threadIdx.x % per == 0)
+      lse2[i] = own ? a.lse[static_cast<long long>(bh) * a.R + row] * kLog2e : top + __log2f(l);
+    __syncthreads();
+    if (t0 < L) {
+#pragma unroll 8
+      for (int i = warp % rw; i < rows; i += rw) {
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(s + static_cast<long long>(r0 + i) * a.cap));
+        const float z = lse2[i] == -INFINITY ? INFINITY : lse2[i];  // a row that sees nothing adds 0
+        sum.x += fast_exp2(x.x - z), sum.y += fast_exp2(x.y - z);
+        sum.z += fast_exp2(x.z - z), sum.w += fast_exp2(x.w - z);
+      }
+    }
+    __syncthreads();
+  }
+  if (rw > 1) {
+    if (warp % rw) part[warp / rw * (rw - 1) + warp % rw - 1][lane] = sum;
+    __syncthreads();
+    if (warp % rw) return;
+    for (int i = 0; i < rw - 1; ++i) {
+      const float4 v = part[warp / rw * (rw - 1) + i][lane];
+      sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+    }
+  }
+  const float add[4] = {sum.x, sum.y, sum.z, sum.w};
+  const long long at = static_cast<long long>(bh) * a.cap + t0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (t0 + k < L) a.mass_out[at + k] = a.mass ? fmaf(a.decay, a.mass[at + k], add[k]) : add[k];
+}
+
 // Joins the partials of the segments that several CTAs share, in their order,
 // and writes the rows of empty sequences.  One CTA a row (blockIdx.y) of a (b, h,
 // row segment): the statistics of all partials first, then D / 4 threads a
-// partial, as many partials at once as fit.
+// partial, as many partials at once as fit.  With a mass, blockIdx.y from seg_rows
+// on are its chunks of tokens (of the key head's first row segment).
 template <int D>
 __global__ void __launch_bounds__(128) cache_attn_combine_kernel(const CacheAttnArgs a,
                                                                  unsigned ctas) {
@@ -832,35 +959,27 @@ __global__ void __launch_bounds__(128) cache_attn_combine_kernel(const CacheAttn
   __shared__ float s_max[4], s_l[4];
   grid_dep_wait();
   const int seg_rows = min(a.R, a.tile * a.wr), rr = blockIdx.y;
-  const int c = (threadIdx.x % TPR) * 4, part = threadIdx.x / TPR, warp = warp_id();
   const int mult = a.Hk * a.row_segs;
   const int b = blockIdx.x / mult, seg = blockIdx.x - b * mult;
   const int h = seg / a.row_segs, rs = seg - h * a.row_segs;
+  if (rr >= seg_rows) {
+    if (rs == 0) add_mass(a, ctas, b * a.Hk + h, rr - seg_rows);
+    return;
+  }
+  const int c = (threadIdx.x % TPR) * 4, part = threadIdx.x / TPR, warp = warp_id();
   const int row = rs * a.wr * a.tile + rr;
   if (row >= a.R) return;
   const long long out = (static_cast<long long>(b) * a.Hk + h) * a.R + row;
-  unsigned before, total;
-  count_blocks(a, b, before, total);
-  const unsigned nb = cache_blocks(a, b);
-  if (nb == 0) {
+  const Parts parts = parts_of(a, b, seg, ctas);
+  const unsigned n = parts.n;
+  if (n == 0) {
     if (part == 0) *reinterpret_cast<uint2*>(a.o + out * D + c) = make_uint2(0, 0);
     if (threadIdx.x == 0) a.lse[out] = -INFINITY;
-    return;
   }
-  const unsigned s0 = before * mult + seg * nb, s1 = s0 + nb;
-  const Cut cut(total * mult, ctas);
-  const unsigned i0 = cut.holder(s0), i1 = cut.holder(s1 - 1);
-  if (i0 == i1) return;  // one CTA had it whole
-  // partial k of i0 .. i1: the CTA's first segment (slot 0), but for one that started before
-  const unsigned n = i1 - i0 + 1;
-  const unsigned late = cut.start(i0) < s0 ? 1u : 0u;
-  const auto index = [&](unsigned k) {
-    return (static_cast<long long>(i0 + k) * 2 + (k == 0 ? late : 0u)) * seg_rows + rr;
-  };
+  if (n <= 1) return;
   float m = -INFINITY;
-  for (unsigned k = threadIdx.x; k < n; k += 128) m = fmaxf(m, a.part_ml[index(k)].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (unsigned k = threadIdx.x; k < n; k += 128) m = fmaxf(m, a.part_ml[parts.index(k, seg_rows, rr)].x);
+  m = warp_max(m);
   if (lane_id() == 0) s_max[warp] = m;
   __syncthreads();
   m = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
@@ -870,7 +989,7 @@ __global__ void __launch_bounds__(128) cache_attn_combine_kernel(const CacheAttn
   for (unsigned k0 = 0; k0 < n; k0 += 128) {
     const unsigned k = k0 + threadIdx.x;
     if (k < n) {
-      const float2 ml = a.part_ml[index(k)];
+      const float2 ml = a.part_ml[parts.index(k, seg_rows, rr)];
       const float f = fast_exp2(ml.x - base);
       weight[threadIdx.x] = f;
       l = fmaf(ml.y, f, l);
@@ -880,14 +999,13 @@ __global__ void __launch_bounds__(128) cache_attn_combine_kernel(const CacheAttn
 #pragma unroll 4
     for (unsigned j = part; j < top; j += PAR) {
       const float f = weight[j];
-      const float4 v = *reinterpret_cast<const float4*>(a.part_o + index(k0 + j) * D + c);
+      const float4 v = *reinterpret_cast<const float4*>(a.part_o + parts.index(k0 + j, seg_rows, rr) * D + c);
       acc.x = fmaf(v.x, f, acc.x), acc.y = fmaf(v.y, f, acc.y);
       acc.z = fmaf(v.z, f, acc.z), acc.w = fmaf(v.w, f, acc.w);
     }
     __syncthreads();
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  l = warp_sum(l);
   if (lane_id() == 0) s_l[warp] = l;
   sum[threadIdx.x] = acc;
   __syncthreads();
@@ -901,34 +1019,6 @@ __global__ void __launch_bounds__(128) cache_attn_combine_kernel(const CacheAttn
   *reinterpret_cast<uint2*>(a.o + out * D + c) =
       make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
   if (c == 0) a.lse[out] = (m + __log2f(l)) * kLn2;
-}
-
-// mass_out = decay mass + sum over the key head's rows of exp(x - LSE), for the
-// tokens of each sequence; 4 tokens a thread.
-__global__ void __launch_bounds__(128) cache_mass_kernel(const CacheAttnArgs a, const float* mass,
-                                                         float* mass_out, float decay) {
-  grid_dep_wait();
-  const int bh = blockIdx.x, b = bh / a.Hk;
-  const int t0 = (blockIdx.y * 128 + threadIdx.x) * 4;
-  const int L = min(a.lengths[b], a.cap);
-  if (t0 >= L) return;
-  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-  const float* s = a.scores + static_cast<long long>(bh) * a.R * a.cap + t0;
-  const float* lse = a.lse + static_cast<long long>(bh) * a.R;
-#pragma unroll 4
-  for (int i = 0; i < a.R; ++i) {
-    const float z = lse[i];
-    if (z == -INFINITY) continue;  // the row sees nothing
-    const float4 x = *reinterpret_cast<const float4*>(s + static_cast<long long>(i) * a.cap);
-    const float y = z * kLog2e;
-    sum.x += fast_exp2(x.x - y), sum.y += fast_exp2(x.y - y);
-    sum.z += fast_exp2(x.z - y), sum.w += fast_exp2(x.w - y);
-  }
-  const float add[4] = {sum.x, sum.y, sum.z, sum.w};
-  const long long at = static_cast<long long>(bh) * a.cap + t0;
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (t0 + k < L) mass_out[at + k] = mass ? fmaf(decay, mass[at + k], add[k]) : add[k];
 }
 
 }  // namespace rfb

@@ -128,7 +128,8 @@ int launch_cache_attn(const CacheAttnArgs& a, const CaPlan& p, cudaStream_t st) 
                  : a.scores  ? launch_cache_attn_main<D, RP, 2, true>(a, p, st)
                              : launch_cache_attn_main<D, RP, 2, false>(a, p, st);
   if (rc != RFB_OK) return rc;
-  const dim3 grid(static_cast<unsigned>(a.B * a.Hk * a.row_segs), p.seg_rows);
+  const dim3 grid(static_cast<unsigned>(a.B * a.Hk * a.row_segs),
+                  p.seg_rows + (a.scores ? (a.cap + mass_tokens(a.R) - 1) / mass_tokens(a.R) : 0));
   launch_pdl(cache_attn_combine_kernel<D>, grid, dim3(128), 0, st, a,
              static_cast<unsigned>(p.ctas));
   return launch_status();
@@ -261,8 +262,8 @@ int rfb_attn_fwd_cache(const void* q, const void* u, const void* k8, const void*
   if (B == 0 || heads == 0 || Nq == 0) return RFB_OK;
   if (heads_kv == 0 || heads % heads_kv != 0) return RFB_ERR_INVALID_ARG;
   const long long R = static_cast<long long>(heads / heads_kv) * Nq;
-  if (R > (1LL << 24) || static_cast<long long>(B) * heads_kv * ((R + 7) / 8) > 0x7fffffffLL / (cap / kCacheBlock + 1) ||
-      (mass_out && cap > 65535 * 512))
+  if (R > (1LL << 24) || static_cast<long long>(B) * heads_kv * ((R + 7) / 8) > 0x7fffffffLL / (cap / kCacheBlock + 8) ||
+      (mass_out && cap > 65000 * 128))
     return RFB_ERR_UNSUPPORTED;
   if (!q || !o || !lse || !lengths || (r > 0 && !u) ||
       (cap > 0 && (!k8 || !v8 || !k_scale || !v_scale || (r > 0 && (!w8 || !w_scale)))))
@@ -292,6 +293,7 @@ int rfb_attn_fwd_cache(const void* q, const void* u, const void* k8, const void*
   a.part_ml = reinterpret_cast<float2*>(ws);
   a.part_o = reinterpret_cast<float*>(ws + p.ml_bytes);
   a.scores = mass_out ? reinterpret_cast<float*>(ws + p.ml_bytes + p.o_bytes) : nullptr;
+  a.mass = mass, a.mass_out = mass_out, a.decay = decay;
   a.B = B, a.Hk = heads_kv, a.R = static_cast<int>(R), a.Nq = Nq, a.cap = cap, a.r = r;
   a.tile = p.tile, a.wr = p.wr, a.row_segs = p.row_segs;
   a.causal = causal;
@@ -301,13 +303,9 @@ int rfb_attn_fwd_cache(const void* q, const void* u, const void* k8, const void*
   a.fail_site = g_fail_site.load();
   a.scale_log2 = scale * kLog2e;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  int rc = d == 32   ? dispatch_cache_attn<32>(a, p, st)
-           : d == 64 ? dispatch_cache_attn<64>(a, p, st)
-                     : dispatch_cache_attn<128>(a, p, st);
-  if (rc != RFB_OK || !mass_out || cap == 0) return rc;
-  const dim3 grid(static_cast<unsigned>(B) * heads_kv, (cap + 511) / 512);
-  launch_pdl(cache_mass_kernel, grid, dim3(128), 0, st, a, mass, mass_out, decay);
-  return launch_status();
+  return d == 32   ? dispatch_cache_attn<32>(a, p, st)
+         : d == 64 ? dispatch_cache_attn<64>(a, p, st)
+                   : dispatch_cache_attn<128>(a, p, st);
 }
 
 int rfb_cache_evict(const void* k8, const void* v8, const void* w8, const float* k_scale,
