@@ -52,10 +52,28 @@ __device__ __forceinline__ uint32_t requantise4(uint32_t v, float ratio) {
   return f32x2_to_e4m3x2(a.x * ratio, a.y * ratio) |
          (f32x2_to_e4m3x2(b.x * ratio, b.y * ratio) << 16);
 }
-// Magnitude codes of four bytes, the NaN code (0x7f) counted as 0.
-__device__ __forceinline__ uint32_t finite_mag4(uint32_t v) {
-  const uint32_t m = v & 0x7f7f7f7fu;
-  return m & ~__vcmpeq4(m, 0x7f7f7f7fu);
+// Larger magnitude of two fp16 pairs, NaN ignored.
+__device__ __forceinline__ uint32_t max_mag_f16x2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmax2(*reinterpret_cast<const __half2*>(&a),
+                            __habs2(*reinterpret_cast<const __half2*>(&b)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t max_mag_e4m3x4(uint32_t top, uint32_t codes) {
+  return max_mag_f16x2(max_mag_f16x2(top, e4m3_lo(codes)), e4m3_hi(codes));
+}
+// Four codes to a scale that is 2^-k times theirs, ratio = (2^k, 2^k) as fp16, k in
+// [-14, 15] and no result above 448.  The product in fp16 is exact, or, where it loses
+// bits, so far below half the smallest code that it becomes zero either way.
+__device__ __forceinline__ uint32_t shift_codes4(uint32_t v, __half2 ratio) {
+  const uint32_t lo = e4m3_lo(v), hi = e4m3_hi(v);
+  const __half2 a = __hmul2(*reinterpret_cast<const __half2*>(&lo), ratio);
+  const __half2 b = __hmul2(*reinterpret_cast<const __half2*>(&hi), ratio);
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e4m3x2.f16x2 lo, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 hi, %2;\n\tmov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(r)
+      : "r"(*reinterpret_cast<const uint32_t*>(&a)), "r"(*reinterpret_cast<const uint32_t*>(&b)));
+  return r;
 }
 
 }  // namespace rfb

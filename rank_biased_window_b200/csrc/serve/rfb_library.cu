@@ -145,6 +145,59 @@ int dispatch_cache_attn(const CacheAttnArgs& a, const CaPlan& p, cudaStream_t st
   }
 }
 
+// Launch with programmatic serialisation and, where cx * cy > 1, in clusters.
+template <typename... KArgs, typename... Args>
+void launch_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, unsigned cx,
+                    unsigned cy, cudaStream_t st, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cx;
+  attr[1].val.clusterDim.y = cy;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cx * cy > 1 ? 2 : 1;
+  (void)cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int KEYS>
+int launch_select(const EvictArgs& a, int parts, cudaStream_t st) {
+  launch_cluster(cache_select_kernel<KEYS>, dim3(a.heads * parts), dim3(kSelThreads), 0, parts, 1,
+                 st, a, parts);
+  return launch_status();
+}
+
+// The move after an eviction.
+template <int D>
+int launch_move(const EvictArgs& a, int sms, cudaStream_t st) {
+  static std::atomic<uint64_t> done[2];
+  constexpr int kMost = kMoveWarps * kMoveStages * move_stage_bytes(D, 64);
+  const int stage = move_stage_bytes(D, a.r), smem = kMoveWarps * kMoveStages * stage;
+  const dim3 block(kMoveWarps * 32);
+  const int wave = sms * (227 * 1024 / (smem + 1024) < 8 ? 227 * 1024 / (smem + 1024) : 8);
+  const int rows_cta = kCacheBlock * kMoveWarps;
+  if (a.in_place) {
+    if (int rc = ensure_smem(cache_move_kernel<D, true>, kMost, done[0])) return rc;
+    // clusters as large as one wave of CTAs (the mass's are short) and the blocks allow
+    int c = 1;
+    while (c < 8 && 2 * c * a.heads * a.tensors <= wave && c * rows_cta < a.keep) c *= 2;
+    launch_cluster(cache_move_kernel<D, true>, dim3(a.heads * (a.tensors + 1), c), block, smem, 1, c,
+                   st, a);
+  } else {
+    if (int rc = ensure_smem(cache_move_kernel<D, false>, kMost, done[1])) return rc;
+    const long long most = 2LL * a.heads * ((a.keep + rows_cta - 1) / rows_cta);
+    launch_pdl(cache_move_kernel<D, false>,
+               dim3(static_cast<unsigned>(most < wave ? most : wave), 3), block, smem, st, a);
+  }
+  return launch_status();
+}
+
 }  // namespace
 }  // namespace rfb
 
@@ -227,7 +280,7 @@ int rfb_cache_append(const void* k, const void* v, const void* w, const long lon
   if (a.blocks > cap / kCacheBlock) a.blocks = cap / kCacheBlock;
   DeviceInfo dev;
   if (int rc = current_device(&dev)) return rc;
-  const long long units = static_cast<long long>(a.blocks) * a.tensors;
+  const long long units = static_cast<long long>(a.blocks) * a.tensors * (d > 64 ? 2 : 1);  // warps
   const dim3 grid(static_cast<unsigned>((units + kAppendWarps - 1) / kAppendWarps), heads_kv, B);
   const dim3 block(kAppendWarps * 32);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -350,26 +403,32 @@ int rfb_cache_evict(const void* k8, const void* v8, const void* w8, const float*
   a.lengths = lengths;
   a.new_lengths = new_lengths;
   a.kept = kept;
-  a.Hk = heads_kv, a.cap = cap, a.to_cap = cap_out, a.d = d, a.r = r;
+  a.heads = B * heads_kv, a.Hk = heads_kv, a.cap = cap, a.to_cap = cap_out, a.d = d, a.r = r;
   a.keep = keep, a.recent = recent;
   DeviceInfo dev;
   if (int rc = current_device(&dev)) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int bh = B * heads_kv;
-  launch_pdl(cache_select_kernel, dim3(bh), dim3(kSelThreads), 0, st, a);
-  if (int rc = launch_status()) return rc;
-  // Out of place, enough parts for two CTAs an SM; in place the blocks go in order.
+  // A cluster of CTAs a (sequence, head) while that leaves SMs without one and
+  // each CTA a few thousand tokens, or where the keys of one do not fit.
   int parts = 1;
-  if (!a.in_place) {
-    const int most = (keep + kCacheBlock * kMoveWarps - 1) / (kCacheBlock * kMoveWarps);
-    const int want = (2 * dev.sms + bh * a.tensors - 1) / (bh * a.tensors);
-    parts = want < most ? want : most;
+  while (parts < 8 && ((2 * parts * bh <= dev.sms && cap > 2048 * parts) ||
+                       cap > parts * kSelMaxKeys * kSelThreads))
+    parts *= 2;
+  const int held = (cap + parts * kSelThreads - 1) / (parts * kSelThreads);
+  int rc = held <= 2    ? launch_select<2>(a, parts, st)
+           : held <= 8  ? launch_select<8>(a, parts, st)
+           : held <= 16 ? launch_select<16>(a, parts, st)
+           : held <= kSelMaxKeys ? launch_select<kSelMaxKeys>(a, parts, st)
+                                 : RFB_ERR_UNSUPPORTED;
+  if (held > kSelMaxKeys) {
+    launch_pdl(cache_select_long_kernel, dim3(bh), dim3(kSelThreads), 0, st, a);
+    rc = launch_status();
   }
-  const dim3 grid(static_cast<unsigned>(bh) * (a.tensors + 1), parts), block(kMoveWarps * 32);
-  if (d == 32) launch_pdl(cache_move_kernel<32>, grid, block, 0, st, a);
-  else if (d == 64) launch_pdl(cache_move_kernel<64>, grid, block, 0, st, a);
-  else launch_pdl(cache_move_kernel<128>, grid, block, 0, st, a);
-  return launch_status();
+  if (rc != RFB_OK) return rc;
+  if (d == 32) return launch_move<32>(a, dev.sms, st);
+  if (d == 64) return launch_move<64>(a, dev.sms, st);
+  return launch_move<128>(a, dev.sms, st);
 }
 
 }  // extern "C"

@@ -130,45 +130,65 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotArgs a) {
   const int total = a.heads[0] + a.heads[1];
   const int h0 = blockIdx.y * a.heads_per_thread;
   const int h1 = min(h0 + a.heads_per_thread, total);
-#pragma unroll 4
-  for (int hh = h0; hh < h1; ++hh) {
-    const int z = hh >= a.heads[0];
-    const int h = z ? hh - a.heads[0] : hh;
-    const T* x = static_cast<const T*>(a.x[z]) + b * a.sb[z] + h * a.sh[z] + n * a.sn[z];
-    T* y = static_cast<T*>(a.y[z]) +
-           ((static_cast<long long>(b) * a.heads[z] + h) * a.N + n) * a.d;
-    if constexpr (VEC_OK) {
-      const uint4 v0 = *reinterpret_cast<const uint4*>(x + c0);
-      if (copy) {
-        *reinterpret_cast<uint4*>(y + c0) = v0;
-      } else if constexpr (HALF) {
-        const uint4 v1 = *reinterpret_cast<const uint4*>(x + c1);
-        float p[V], q[V], o0[V], o1[V];
-        R::load(v0, p);
-        R::load(v1, q);
+  const auto in = [&](int hh) {
+    const int z = hh >= a.heads[0], h = z ? hh - a.heads[0] : hh;
+    return static_cast<const T*>(a.x[z]) + b * a.sb[z] + h * a.sh[z] + n * a.sn[z];
+  };
+  const auto out = [&](int hh) {
+    const int z = hh >= a.heads[0], h = z ? hh - a.heads[0] : hh;
+    return static_cast<T*>(a.y[z]) + ((static_cast<long long>(b) * a.heads[z] + h) * a.N + n) * a.d;
+  };
+  if constexpr (VEC_OK) {
+    // the loads of BATCH heads go out before the first of their stores
+    constexpr int BATCH = HALF ? 2 : 4;
+    for (int hh = h0; hh < h1; hh += BATCH) {
+      uint4 v0[BATCH], v1[BATCH];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          o0[i] = p[i] * cs[i] - q[i] * sn[i];
-          o1[i] = q[i] * cs[i] + p[i] * sn[i];
-        }
-        *reinterpret_cast<uint4*>(y + c0) = R::store(o0);
-        *reinterpret_cast<uint4*>(y + c1) = R::store(o1);
-      } else {
-        float p[V], o[V];
-        R::load(v0, p);
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-          o[2 * i] = p[2 * i] * cs[i] - p[2 * i + 1] * sn[i];
-          o[2 * i + 1] = p[2 * i + 1] * cs[i] + p[2 * i] * sn[i];
-        }
-        *reinterpret_cast<uint4*>(y + c0) = R::store(o);
+      for (int k = 0; k < BATCH; ++k) {
+        if (hh + k >= h1) break;
+        v0[k] = __ldcs(reinterpret_cast<const uint4*>(in(hh + k) + c0));
+        if (HALF && !copy) v1[k] = __ldcs(reinterpret_cast<const uint4*>(in(hh + k) + c1));
       }
-    } else if (copy) {
-      y[c0] = x[c0];
-    } else {
-      const float p = R::one(x[c0]), q = R::one(x[c1]);
-      y[c0] = R::to(p * cs[0] - q * sn[0]);
-      y[c1] = R::to(q * cs[0] + p * sn[0]);
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) {
+        if (hh + k >= h1) break;
+        T* y = out(hh + k);
+        if (copy) {
+          *reinterpret_cast<uint4*>(y + c0) = v0[k];
+        } else if constexpr (HALF) {
+          float p[V], q[V], o0[V], o1[V];
+          R::load(v0[k], p);
+          R::load(v1[k], q);
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            o0[i] = p[i] * cs[i] - q[i] * sn[i];
+            o1[i] = q[i] * cs[i] + p[i] * sn[i];
+          }
+          *reinterpret_cast<uint4*>(y + c0) = R::store(o0);
+          *reinterpret_cast<uint4*>(y + c1) = R::store(o1);
+        } else {
+          float p[V], o[V];
+          R::load(v0[k], p);
+#pragma unroll
+          for (int i = 0; i < V / 2; ++i) {
+            o[2 * i] = p[2 * i] * cs[i] - p[2 * i + 1] * sn[i];
+            o[2 * i + 1] = p[2 * i + 1] * cs[i] + p[2 * i] * sn[i];
+          }
+          *reinterpret_cast<uint4*>(y + c0) = R::store(o);
+        }
+      }
+    }
+  } else {
+    for (int hh = h0; hh < h1; ++hh) {
+      const T* x = in(hh);
+      T* y = out(hh);
+      if (copy) {
+        y[c0] = x[c0];
+      } else {
+        const float p = R::one(x[c0]), q = R::one(x[c1]);
+        y[c0] = R::to(p * cs[0] - q * sn[0]);
+        y[c1] = R::to(q * cs[0] + p * sn[0]);
+      }
     }
   }
 }
