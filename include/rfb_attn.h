@@ -368,9 +368,10 @@ RFB_API int rfb_cache_append(const void* k, const void* v, const void* w, const 
  *       t < lengths[b]; mass may be mass_out (in place) or NULL (zeros).
  *   workspace : device, 16-byte aligned, at least
  *       rfb_attn_fwd_cache_workspace_size() bytes, as for rfb_attn_bwd (with
- *       mass_out it holds the scores, 4 bytes a query row and token of capacity).
+ *       mass_out and up to 8 query rows a key head it holds their scores, 4 bytes
+ *       a row and token of capacity).
  * heads a multiple of heads_kv; made for steps of one to some dozens of tokens
- * (a longer prompt is read once per 64 query rows).
+ * (the cache is read once per 64 query rows of a key head).
  */
 RFB_API size_t rfb_attn_fwd_cache_workspace_size(int B, int heads, int heads_kv, int Nq, int cap,
                                                  int d, int with_mass);

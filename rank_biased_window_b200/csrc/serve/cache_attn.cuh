@@ -11,8 +11,9 @@
 // match), become fp16 there (exact) and enter m16n8k16 MMAs with fp32
 // accumulators.  Softmax statistics and sums are fp32; the probabilities are
 // rounded to fp16 for the product with V (2^-11 relative, below the bf16
-// rounding of O), lifted by 2^15 so that this holds down to 2^-29 of the largest:
-// a token of small weight may have a large value.  Queries enter as fp16 scaled by a power of two per row,
+// rounding of O), lifted by 2^11 so that this holds down to 2^-25 of the largest:
+// a token of small weight may have a large value.  The largest is followed with a slack of 2^4,
+// so that the sums are rescaled a few times a segment (2^15 is within fp16).  Queries enter as fp16 scaled by a power of two per row,
 // which holds every bf16 within 2^-29 of the row's largest exactly.
 //
 // Bound by HBM: 2 d + r bytes a token and head.  With at most 16 rows in a
@@ -35,7 +36,8 @@ namespace rfb {
 constexpr int kCaWarps = 4;
 constexpr int kCaThreads = kCaWarps * 32;
 constexpr unsigned kCaSegmentCost = 4;
-constexpr float kCaLift = 15.f;  // weights are held as 2^(x - max + 15)
+constexpr float kCaLift = 11.f;   // weights are held as 2^(x - max + 11) ...
+constexpr float kCaSlack = 4.f;   // ... with a max that scores may pass by 2^4 before it moves
 
 struct CacheAttnArgs {
   const __nv_bfloat16* q;  // [B, Hk, R, d], R = group * Nq
@@ -205,19 +207,26 @@ __device__ __forceinline__ int factor_channel(int i, int t) {
   return t * (C / 4) + i * 4;
 }
 
-// One query row of C bf16 channels (lane g's, its t-th pieces) as fp16 B
-// fragments, times 2^(14 - e) with e the exponent of its largest; returns 2^(e - 14).
+// One query row of C bf16 channels, the lane's t-th pieces.
 template <int C, bool FACTOR>
-__device__ __forceinline__ float load_row(const __nv_bfloat16* x, int channels, bool live, int t,
-                                          uint32_t (*frag)[2]) {
-  float f[C / 4], top = 0.f;
+__device__ __forceinline__ void fetch_row(const __nv_bfloat16* x, int channels, bool live, int t,
+                                          uint2* raw) {
 #pragma unroll
   for (int i = 0; i < C / 16; ++i) {
     const int ch = FACTOR ? factor_channel<C>(i, t) : piece_channel<C>(i, t);
-    uint2 v = make_uint2(0, 0);
-    if (live && ch < channels) v = __ldg(reinterpret_cast<const uint2*>(x + ch));
-    const float e[4] = {__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u),
-                        __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u)};
+    raw[i] = make_uint2(0, 0);
+    if (live && ch < channels) raw[i] = __ldg(reinterpret_cast<const uint2*>(x + ch));
+  }
+}
+// The row as fp16 B fragments, times 2^(14 - e) with e the exponent of its largest;
+// returns 2^(e - 14).
+template <int C>
+__device__ __forceinline__ float row_fragments(const uint2* raw, uint32_t (*frag)[2]) {
+  float f[C / 4], top = 0.f;
+#pragma unroll
+  for (int i = 0; i < C / 16; ++i) {
+    const float e[4] = {__uint_as_float(raw[i].x << 16), __uint_as_float(raw[i].x & 0xffff0000u),
+                        __uint_as_float(raw[i].y << 16), __uint_as_float(raw[i].y & 0xffff0000u)};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       f[4 * i + k] = e[k];
@@ -430,6 +439,13 @@ __global__ void __launch_bounds__(kCaThreads, 3)
   int in_stage = 0, in_phase = 0, out_stage = 0, out_phase = 0;
   int loads = 0;   // copies this warp started (the ring's s-th stage got loads s, s + stages, ...)
   int issued = 0;  // blocks of this segment (and the next) loaded by this group so far
+  // lanes 0, 1, 2 copy K, V, W; each keeps where its next block starts
+  const bool copies = lane < (RP > 0 ? 3 : 2);
+  const uint8_t* const my_base = lane == 0 ? a.k : lane == 1 ? a.v : a.w;
+  const float* const my_scales = lane == 0 ? a.ks : lane == 1 || RP == 0 ? a.vs : a.ws;
+  const unsigned my_width = lane < 2 ? D : a.r, my_bytes = kCacheBlock * my_width;
+  const unsigned my_step = wts * my_bytes;
+  const uint8_t* src = nullptr;
 
   while (at < stop) {
     const int h = seg / a.row_segs, rs = seg - h * a.row_segs;
@@ -451,32 +467,46 @@ __global__ void __launch_bounds__(kCaThreads, 3)
     const int ahead = mine + max(nblk1 - wt + wts - 1, 0) / wts;    // and with the next segment's
     const long long nbh = static_cast<long long>(nxb) * a.Hk + nseg / a.row_segs;
 
+    if (first) src = my_base + (bh * a.cap + (blk0 + wt) * kCacheBlock) * my_width;
+    const uint8_t* const next_src = my_base + (nbh * a.cap + wt * kCacheBlock) * my_width;
+    if (issued == mine) src = next_src;
     // Loads blocks until `upto` of them (counted from this segment's first) are under way.
     const auto pump = [&](int upto) {
-      while (issued < min(upto, ahead)) {
+      for (upto = min(upto, ahead); issued < upto;) {
         if (leader && !dead) {
-          const bool here = issued < mine;
-          const long long tok =
-              (here ? bh : nbh) * a.cap +
-              static_cast<long long>(here ? blk0 + wt + issued * wts : wt + (issued - mine) * wts) *
-                  kCacheBlock;
           bool ok = true;
           if (a.wr > 1) ok = wait_warp(empty + 8 * in_stage, in_phase ^ 1, guard, 70);
           if (!ok) dead = true;
-          if (ok && lane == 0) {
-            const uint32_t bar = full + 8 * in_stage, dst = ring + in_stage * stage_bytes;
-            mbar_expect_tx(bar, stage_bytes);
-            bulk_load(dst, a.k + tok * D, v_off, bar);
-            bulk_load(dst + v_off, a.v + tok * D, v_off, bar);
-            if constexpr (RP > 0) bulk_load(dst + w_off, a.w + tok * a.r, w_bytes, bar);
+          if (ok) {
+            const uint32_t bar = full + 8 * in_stage;
+            if (lane == 0) mbar_expect_tx(bar, stage_bytes);
+            if (copies) bulk_load(ring + in_stage * stage_bytes + lane * v_off, src, my_bytes, bar);
           }
           loads += ok;
         }
         if (++in_stage == stages) in_stage = 0, in_phase ^= 1;
-        ++issued;
+        src = ++issued == mine ? next_src : src + my_step;
       }
     };
-    pump(stages);
+    // The queries are asked for before the blocks: behind a ring full of them they
+    // would wait for all of it.
+    uint2 raw_q[QT][KW], raw_u[QT][WW > 0 ? WW : 1];
+    if (blk0 < blk1) {
+#pragma unroll
+      for (int q = 0; q < QT; ++q) {
+        const int row = row0 + 8 * q + g;
+        fetch_row<D, false>(a.q + (bh * a.R + row) * D, D, row < a.R, t, raw_q[q]);
+        if constexpr (RP > 0)
+          fetch_row<RP, true>(a.u + (bh * a.R + row) * a.r, a.r, row < a.R, t, raw_u[q]);
+      }
+    }
+    // the block's scales, one in each of lanes 0, 1, 2
+    const float* scales = my_scales + bh * (a.cap / kCacheBlock) + blk0 + wt;
+    float scale = 0.f;
+    if (copies && mine > 0) scale = __ldg(scales);
+    // One block a group at first: a ring asked for whole at the start comes in the
+    // order of the asking, and its last stages would hold up the others' first ones.
+    pump(max(issued, 1));
     if (blk0 == blk1) break;  // only at the end of the part
 
     // Queries as B fragments (lane g: query g of each tile); scores, sums and O are
@@ -487,11 +517,9 @@ __global__ void __launch_bounds__(kCaThreads, 3)
 #pragma unroll
     for (int q = 0; q < QT; ++q) {
       const int row = row0 + 8 * q + g;
-      const float f = load_row<D, false>(a.q + (bh * a.R + row) * D, D, row < a.R, t, qf[q]) *
-                      a.scale_log2;
+      const float f = row_fragments<D>(raw_q[q], qf[q]) * a.scale_log2;
       float e = 0.f;
-      if constexpr (RP > 0)
-        e = load_row<RP, true>(a.u + (bh * a.R + row) * a.r, a.r, row < a.R, t, uf[q]) * kLog2e;
+      if constexpr (RP > 0) e = row_fragments<RP>(raw_u[q], uf[q]) * kLog2e;
       int n = L;
       if (a.causal && row < a.R) n = max(min(L, L - a.Nq + 1 + row % a.Nq), 0);
       lim_lo = min(lim_lo, n);
@@ -505,10 +533,13 @@ __global__ void __launch_bounds__(kCaThreads, 3)
     }
     lim_lo = __reduce_min_sync(0xffffffffu, lim_lo);
 
-    float m[QT][2], l[QT][2], oacc[NT][QT][4];
+    // Weights are 2^(x - m), m the largest score up to a slack, less the lift: m moves (and
+    // with it the sums) only when a score passes `over`.
+    float m[QT][2], over[QT][2], l[QT][2], oacc[NT][QT][4];
 #pragma unroll
     for (int q = 0; q < QT; ++q) {
-      m[q][0] = m[q][1] = -INFINITY;
+      m[q][0] = m[q][1] = 0.f;
+      over[q][0] = over[q][1] = -INFINITY;
       l[q][0] = l[q][1] = 0.f;
 #pragma unroll
       for (int i = 0; i < NT; ++i)
@@ -517,22 +548,18 @@ __global__ void __launch_bounds__(kCaThreads, 3)
     }
     float unit = 1.f;  // oacc is O / unit
 
-    const long long sbase = bh * (a.cap / kCacheBlock);
-    float ksc = 1.f, vsc = 1.f, wsc = 0.f;
-    const auto load_scales = [&](int blk) {
-      ksc = __ldg(a.ks + sbase + blk);
-      vsc = __ldg(a.vs + sbase + blk);
-      if constexpr (RP > 0) wsc = __ldg(a.ws + sbase + blk);
-    };
-    if (mine > 0) load_scales(blk0 + wt);
+    pump(max(issued, 2));
     uint32_t held = 0;  // stage of the segment's last block: the warps join through it
 
     for (int i = 0; i < mine; ++i) {
       const int blk = blk0 + wt + i * wts;
       if (!wait_warp(full + 8 * out_stage, out_phase, guard, 71)) dead = true;
       const uint32_t st = ring + out_stage * stage_bytes;
-      const float ks_now = ksc, vs_now = vsc, ws_now = wsc;
-      if (i + 1 < mine) load_scales(blk + wts);
+      const float ks_now = __shfl_sync(0xffffffffu, scale, 0);
+      const float vs_now = __shfl_sync(0xffffffffu, scale, 1);
+      const float ws_now = RP > 0 ? __shfl_sync(0xffffffffu, scale, 2) : 0.f;
+      scales += wts;
+      if (copies && i + 1 < mine) scale = __ldg(scales);
       // scores in units of log2: x[j][q] of tokens g, g + 8 of half j (as tile_token
       // orders them) and queries 2 t, 2 t + 1
       float x[2][QT][4];
@@ -630,19 +657,14 @@ __global__ void __launch_bounds__(kCaThreads, 3)
             }
           }
       }
-      // running maximum and sum
       float mx[QT][2];
       bool moved = vs_now != unit;
 #pragma unroll
       for (int q = 0; q < QT; ++q)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float v = fmax3(m[q][e], x[0][q][e], x[0][q][2 + e]);
-          v = fmax3(v, x[1][q][e], x[1][q][2 + e]);
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-          mx[q][e] = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-          moved |= mx[q][e] != m[q][e];
+          mx[q][e] = fmaxf(fmax3(x[0][q][e], x[0][q][2 + e], x[1][q][e]), x[1][q][2 + e]);
+          moved |= mx[q][e] > over[q][e];
         }
       if (__any_sync(0xffffffffu, moved)) {
         const float back = unit / vs_now;
@@ -652,8 +674,16 @@ __global__ void __launch_bounds__(kCaThreads, 3)
           float al[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            al[e] = mx[q][e] == -INFINITY ? 1.f : fast_exp2(m[q][e] - mx[q][e]);
-            m[q][e] = mx[q][e];
+            float v = mx[q][e];
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+            al[e] = 1.f;
+            if (v > over[q][e]) {
+              v -= kCaLift;
+              al[e] = over[q][e] == -INFINITY ? 0.f : fast_exp2(m[q][e] - v);
+              m[q][e] = v;
+              over[q][e] = v + (kCaLift + kCaSlack);
+            }
             l[q][e] *= al[e];
             al[e] *= back;
           }
@@ -666,13 +696,11 @@ __global__ void __launch_bounds__(kCaThreads, 3)
       uint32_t p[2][QT][2];
 #pragma unroll
       for (int q = 0; q < QT; ++q) {
-        const float base[2] = {m[q][0] == -INFINITY ? 0.f : m[q][0] - kCaLift,
-                               m[q][1] == -INFINITY ? 0.f : m[q][1] - kCaLift};
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            x[j][q][k] = fast_exp2(x[j][q][k] - base[k & 1]);
+            x[j][q][k] = fast_exp2(x[j][q][k] - m[q][k & 1]);
             l[q][k & 1] += x[j][q][k];
           }
           p[j][q][0] = transpose8x8(pack_f16x2(x[j][q][0], x[j][q][1]));
@@ -696,7 +724,7 @@ __global__ void __launch_bounds__(kCaThreads, 3)
       if (a.wr > 1 && lane == 0 && i + 1 < mine) mbar_arrive(empty + 8 * out_stage);
       if (i + 1 < mine) {
         if (++out_stage == stages) out_stage = 0, out_phase ^= 1;
-        pump(i + 1 + stages);
+        pump(min(i + 1 + stages, 2 * i + 4));
       }
     }
 
@@ -715,9 +743,12 @@ __global__ void __launch_bounds__(kCaThreads, 3)
 #pragma unroll
         for (int k = 0; k < 4; ++k) oacc[n][q][k] *= unit;
     }
-    // from here on m is what the sums are relative to
+    // rows that saw nothing
 #pragma unroll
-    for (int q = 0; q < QT; ++q) m[q][0] -= kCaLift, m[q][1] -= kCaLift;
+    for (int q = 0; q < QT; ++q)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (over[q][e] == -INFINITY) m[q][e] = -INFINITY;
     const bool whole = blk0 == 0 && blk1 == nb;
     const int slot = first ? 0 : 1;
     if (wts > 1) {
@@ -731,6 +762,7 @@ __global__ void __launch_bounds__(kCaThreads, 3)
       }
       __syncthreads();
       const uint32_t buf = head.held[a.wr == 1 ? wt : wr];
+      static_assert(QT <= 2, "O of a warp has to fit into a stage's K and V");
       if (wt > 0 && mine > 0) {
 #pragma unroll
         for (int q = 0; q < QT; ++q)
@@ -872,62 +904,70 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Warps of a mass CTA that share tokens, each with every mass_row_warps-th row.
+// LSE in log2 units of the up to 8 rows of key head bh, joined from the partials
+// again, so that the mass needs no kernel behind the join of O; +inf for rows that
+// see nothing, whose weights are 0.  All 128 threads call it.
+__device__ __forceinline__ void join_lse(const CacheAttnArgs& a, unsigned ctas, int bh, float* lse2) {
+  const int b = bh / a.Hk, h = bh - b * a.Hk;
+  const Parts parts = parts_of(a, b, h, ctas);
+  const int row = threadIdx.x / 16, lane = threadIdx.x % 16;
+  if (row >= a.R) return;  // whole half warps leave together
+  const unsigned half = 0xffffu << (threadIdx.x & 16);
+  float z;
+  if (parts.n == 1) {
+    z = __ldcg(a.lse + static_cast<long long>(bh) * a.R + row) * kLog2e;
+  } else {
+    float m = -INFINITY, l = 0.f;
+#pragma unroll 4
+    for (unsigned k = lane; k < parts.n; k += 16) {
+      const float2 ml = __ldcg(a.part_ml + parts.index(k, a.R, row));
+      const float mn = fmaxf(m, ml.x), base = mn == -INFINITY ? 0.f : mn;
+      l = l * fast_exp2(m - base) + ml.y * fast_exp2(ml.x - base);
+      m = mn;
+    }
+    float top = m;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(half, top, o));
+    l *= fast_exp2(m - (top == -INFINITY ? 0.f : top));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) l += __shfl_xor_sync(half, l, o);
+    z = top + __log2f(l);
+  }
+  if (lane == 0) lse2[row] = z == -INFINITY ? INFINITY : z;
+}
+
+__device__ __forceinline__ void store_mass(const CacheAttnArgs& a, long long at, float add) {
+  a.mass_out[at] = a.mass ? fmaf(a.decay, a.mass[at], add) : add;
+}
+
+// mass_out = decay mass + sum over the key head's rows of exp(x - LSE).  Up to 8
+// rows leave their scores in the workspace (8 bytes of traffic a row and token, less
+// than reading K again); with more rows the scores are computed again.
+
+// From the scores: the warps of a CTA that share tokens take every
+// mass_row_warps-th row each.
 __host__ __device__ __forceinline__ int mass_row_warps(int R) { return R >= 4 ? 4 : R >= 2 ? 2 : 1; }
 __host__ __device__ __forceinline__ int mass_tokens(int R) { return 512 / mass_row_warps(R); }
 
-// mass_out = decay mass + sum over the key head's rows of exp(x - LSE) for
-// mass_tokens of key head bh, 4 a thread.  LSE is joined here again from the
-// partials, so that this needs no kernel behind the join of O.
 __device__ __forceinline__ void add_mass(const CacheAttnArgs& a, unsigned ctas, int bh, int chunk) {
-  __shared__ float lse2[128];  // of 128 rows, in log2 units
+  __shared__ float lse2[8];
   __shared__ float4 part[3][32];
-  const int b = bh / a.Hk, h = bh - b * a.Hk, seg_tile = a.wr * a.tile;
   const int rw = mass_row_warps(a.R), warp = warp_id(), lane = lane_id();
   const int t0 = chunk * mass_tokens(a.R) + (warp / rw) * 128 + lane * 4;
-  const int L = min(a.lengths[b], a.cap);
+  const int L = min(a.lengths[bh / a.Hk], a.cap);
   if (chunk * mass_tokens(a.R) >= L) return;
-  const int seg_rows = min(a.R, a.tile * a.wr);
+  join_lse(a, ctas, bh, lse2);
+  __syncthreads();
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
   const float* s = a.scores + static_cast<long long>(bh) * a.R * a.cap + t0;
-  for (int r0 = 0; r0 < a.R; r0 += 128) {
-    const int rows = min(128, a.R - r0);
-    // lanes that share a row: 32 for up to 4 rows, 1 for 128
-    int per = 32;
-    while (per * rows > 128) per >>= 1;
-    const int i = threadIdx.x / per, row = r0 + i, rs = row / seg_tile;
-    float m = -INFINITY, l = 0.f;
-    bool own = false;
-    for (int r = r0 / seg_tile; r <= (r0 + rows - 1) / seg_tile; ++r) {
-      const Parts parts = parts_of(a, b, h * a.row_segs + r, ctas);
-      if (i >= rows || rs != r) continue;
-      own = parts.n == 1;
-      if (own) continue;
-#pragma unroll 4
-      for (unsigned k = threadIdx.x % per; k < parts.n; k += per) {
-        const float2 ml = a.part_ml[parts.index(k, seg_rows, row - rs * seg_tile)];
-        const float mn = fmaxf(m, ml.x), base = mn == -INFINITY ? 0.f : mn;
-        l = l * fast_exp2(m - base) + ml.y * fast_exp2(ml.x - base);
-        m = mn;
-      }
-    }
-    float top = m;
-    for (int o = per >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    l *= fast_exp2(m - (top == -INFINITY ? 0.f : top));
-    for (int o = per >> 1; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    if (i < rows && threadIdx.x % per == 0)
-      lse2[i] = own ? a.lse[static_cast<long long>(bh) * a.R + row] * kLog2e : top + __log2f(l);
-    __syncthreads();
-    if (t0 < L) {
+  if (t0 < L) {
 #pragma unroll 8
-      for (int i = warp % rw; i < rows; i += rw) {
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(s + static_cast<long long>(r0 + i) * a.cap));
-        const float z = lse2[i] == -INFINITY ? INFINITY : lse2[i];  // a row that sees nothing adds 0
-        sum.x += fast_exp2(x.x - z), sum.y += fast_exp2(x.y - z);
-        sum.z += fast_exp2(x.z - z), sum.w += fast_exp2(x.w - z);
-      }
+    for (int i = warp % rw; i < a.R; i += rw) {
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(s + static_cast<long long>(i) * a.cap));
+      const float z = lse2[i];
+      sum.x += fast_exp2(x.x - z), sum.y += fast_exp2(x.y - z);
+      sum.z += fast_exp2(x.z - z), sum.w += fast_exp2(x.w - z);
     }
-    __syncthreads();
   }
   if (rw > 1) {
     if (warp % rw) part[warp / rw * (rw - 1) + warp % rw - 1][lane] = sum;
@@ -939,46 +979,279 @@ __device__ __forceinline__ void add_mass(const CacheAttnArgs& a, unsigned ctas, 
     }
   }
   const float add[4] = {sum.x, sum.y, sum.z, sum.w};
-  const long long at = static_cast<long long>(bh) * a.cap + t0;
 #pragma unroll
   for (int k = 0; k < 4; ++k)
-    if (t0 + k < L) a.mass_out[at + k] = a.mass ? fmaf(a.decay, a.mass[at + k], add[k]) : add[k];
+    if (t0 + k < L) store_mass(a, static_cast<long long>(bh) * a.cap + t0 + k, add[k]);
 }
 
-// Joins the partials of the segments that several CTAs share, in their order,
-// and writes the rows of empty sequences.  One CTA a row (blockIdx.y) of a (b, h,
-// row segment): the statistics of all partials first, then D / 4 threads a
-// partial, as many partials at once as fit.  With a mass, blockIdx.y from seg_rows
-// on are its chunks of tokens (of the key head's first row segment).
+// Computed again, in a kernel of its own: a warp holds a block of 32 tokens of K
+// (and W) as MMA row operands and goes over all rows, 64 at a time from shared memory,
+// as the main kernel does but with the final LSE; the weights of a token add up over
+// the lanes of its row.  Everything but the LSE was there before the main kernel began
+// and is prepared before the wait for the join.
+constexpr int kMassChunk = 4 * kCacheBlock;
+
+// Pieces of `e4m3 rows` (two, tile_token(g) and 8 behind) of C channels as the MMA's row operand.
+template <int W>
+__device__ __forceinline__ void row_operand(const uint32_t (*r)[W], uint32_t (*f)[4]) {
+#pragma unroll
+  for (int k = 0; k < W; ++k) {
+    f[k][0] = e4m3_lo(r[0][k]), f[k][1] = e4m3_lo(r[1][k]);
+    f[k][2] = e4m3_hi(r[0][k]), f[k][3] = e4m3_hi(r[1][k]);
+  }
+}
+
+template <int D, int RP>
+__global__ void __launch_bounds__(128) cache_mass_kernel(const CacheAttnArgs a) {
+  constexpr int KW = D / 16, WW = RP / 16;
+  __shared__ uint2 sq[8][KW][32], su[WW > 0 ? 8 : 1][WW > 0 ? WW : 1][32];
+  __shared__ float sf[64], sg[64], lse2[64];
+  __shared__ int slim[64];
+  const int bh = blockIdx.x, chunk = blockIdx.y;
+  const int b = bh / a.Hk, warp = warp_id(), lane = lane_id(), g = lane >> 2, t = lane & 3;
+  const int L = min(a.lengths[b], a.cap);
+  if (chunk * kMassChunk >= L) {
+    grid_dep_wait();
+    return;
+  }
+  const int blk = chunk * 4 + warp, tok0 = blk * kCacheBlock;
+  const bool busy = tok0 < L;
+  // the block, on its way while the rows are prepared
+  uint32_t kr[2][2][KW], wr[2][2][WW > 0 ? WW : 1];
+  float ks = 0.f, ws = 0.f;
+  if (busy) {
+    const long long line = static_cast<long long>(bh) * a.cap + tok0;
+    const long long sat = static_cast<long long>(bh) * (a.cap / kCacheBlock) + blk;
+    ks = __ldg(a.ks + sat);
+    if constexpr (RP > 0) ws = __ldg(a.ws + sat);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const long long row = line + 16 * j + 8 * e + tile_token(g);
+        const uint8_t* p = a.k + row * D;
+        if constexpr (D >= 64) {
+#pragma unroll
+          for (int c = 0; c < KW / 4; ++c) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(p + 64 * c + 16 * t));
+            kr[j][e][4 * c] = v.x, kr[j][e][4 * c + 1] = v.y;
+            kr[j][e][4 * c + 2] = v.z, kr[j][e][4 * c + 3] = v.w;
+          }
+        } else {
+          const uint2 v = __ldg(reinterpret_cast<const uint2*>(p + 8 * t));
+          kr[j][e][0] = v.x, kr[j][e][1] = v.y;
+        }
+        if constexpr (RP > 0) {
+          p = a.w + row * a.r;
+#pragma unroll
+          for (int k = 0; k < WW; ++k) wr[j][e][k] = 0;
+          if constexpr (RP == 16) {
+            if (4 * t < a.r) wr[j][e][0] = __ldg(reinterpret_cast<const uint32_t*>(p + 4 * t));
+          } else {
+#pragma unroll
+            for (int k = 0; k < WW / 2; ++k) {
+              const int ch = factor_channel<RP>(2 * k, t);
+              if (ch < a.r) {
+                const uint2 v = __ldg(reinterpret_cast<const uint2*>(p + ch));
+                wr[j][e][2 * k] = v.x, wr[j][e][2 * k + 1] = v.y;
+              }
+            }
+          }
+        }
+      }
+  }
+  float sum[2][2] = {};
+  for (int r0 = 0; r0 < a.R; r0 += 64) {
+    const int rows = min(64, a.R - r0);
+    if (r0 > 0) __syncthreads();  // the rows before have been read
+    uint2 raw[2][KW], raw_u[2][WW > 0 ? WW : 1];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const long long row = r0 + 8 * (warp + 4 * i) + g, line = static_cast<long long>(bh) * a.R + row;
+      fetch_row<D, false>(a.q + line * D, D, row < a.R, t, raw[i]);
+      if constexpr (RP > 0) fetch_row<RP, true>(a.u + line * a.r, a.r, row < a.R, t, raw_u[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int q = warp + 4 * i, row = r0 + 8 * q + g;
+      uint32_t frag[KW][2], uf[WW > 0 ? WW : 1][2];
+      const float f = row_fragments<D>(raw[i], frag) * a.scale_log2;
+#pragma unroll
+      for (int k = 0; k < KW; ++k) sq[q][k][lane] = make_uint2(frag[k][0], frag[k][1]);
+      float e = 0.f;
+      if constexpr (RP > 0) {
+        e = row_fragments<RP>(raw_u[i], uf) * kLog2e;
+#pragma unroll
+        for (int k = 0; k < WW; ++k) su[q][k][lane] = make_uint2(uf[k][0], uf[k][1]);
+      }
+      if (t == 0) {
+        const bool live = row < a.R;
+        sf[8 * q + g] = f;
+        sg[8 * q + g] = e;
+        // a row that is none sees nothing
+        slim[8 * q + g] = !live ? 0 : a.causal ? max(min(L, L - a.Nq + 1 + row % a.Nq), 0) : L;
+      }
+    }
+    if (r0 == 0) grid_dep_wait();  // the rows' LSE
+    if (threadIdx.x < 64) {
+      const float z = threadIdx.x < rows
+                          ? __ldcg(a.lse + static_cast<long long>(bh) * a.R + r0 + threadIdx.x) * kLog2e
+                          : INFINITY;
+      lse2[threadIdx.x] = z == -INFINITY ? INFINITY : z;
+    }
+    __syncthreads();
+    if (!busy) continue;
+    const int tiles = (rows + 7) / 8;
+    uint32_t af[2][KW][4], wf[2][WW > 0 ? WW : 1][4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      row_operand<KW>(kr[j], af[j]);
+      if constexpr (RP > 0) row_operand<WW>(wr[j], wf[j]);
+    }
+#pragma unroll 2
+    for (int q = 0; q < tiles; ++q) {
+      const int row = 8 * q + 2 * t;
+      const float f[2] = {sf[row] * ks, sf[row + 1] * ks};
+      const float z[2] = {lse2[row], lse2[row + 1]};
+      const int lim[2] = {slim[row], slim[row + 1]};
+      float x[2][4] = {};
+#pragma unroll
+      for (int k = 0; k < KW; ++k) {
+        const uint2 v = sq[q][k][lane];
+        mma_f16(x[0], af[0][k], v.x, v.y);
+        mma_f16(x[1], af[1][k], v.x, v.y);
+      }
+      if constexpr (RP > 0) {
+        float cw[2][4] = {};
+#pragma unroll
+        for (int k = 0; k < WW; ++k) {
+          const uint2 v = su[q][k][lane];
+          mma_f16(cw[0], wf[0][k], v.x, v.y);
+          mma_f16(cw[1], wf[1][k], v.x, v.y);
+        }
+        const float e[2] = {sg[row] * ws, sg[row + 1] * ws};
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[j][k] = fmaf(cw[j][k], e[k & 1], x[j][k] * f[k & 1]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[j][k] *= f[k & 1];
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const bool sees = tok0 + 16 * j + 8 * (k >> 1) + tile_token(g) < lim[k & 1];
+          sum[j][k >> 1] += sees ? fast_exp2(x[j][k] - z[k & 1]) : 0.f;
+        }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float v = sum[j][e];
+      v += __shfl_xor_sync(0xffffffffu, v, 1);
+      v += __shfl_xor_sync(0xffffffffu, v, 2);
+      const int tok = tok0 + 16 * j + 8 * e + tile_token(g);
+      if (t == 0 && tok < L) store_mass(a, static_cast<long long>(bh) * a.cap + tok, v);
+    }
+}
+
+// Rows of a CTA of the join: with up to 8 rows a segment one, whose partials go to
+// D / 4 threads each, as many at once as fit; with more, as many rows as fit, each
+// going over its partials in turn.
+__host__ __device__ __forceinline__ int join_rows(int seg_rows, int d) {
+  return seg_rows <= 8 ? 1 : 128 / (d / 4);
+}
+
 template <int D>
-__global__ void __launch_bounds__(128) cache_attn_combine_kernel(const CacheAttnArgs a,
-                                                                 unsigned ctas) {
+__device__ __forceinline__ void store_row(const CacheAttnArgs& a, long long out, int c, float m,
+                                          float l, float4 acc) {
+  const float inv = l > 0.f ? 1.f / l : l;
+  *reinterpret_cast<uint2*>(a.o + out * D + c) =
+      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (c == 0) a.lse[out] = (m + __log2f(l)) * kLn2;
+}
+
+// Joins the partials of a (b, h, row segment) that several CTAs share, in their
+// order; writes the rows of an empty sequence.
+template <int D>
+__device__ __forceinline__ void join_many(const CacheAttnArgs& a, const Parts& parts, int bh, int rs,
+                                          int first) {
+  constexpr int TPR = D / 4;
+  const int seg_rows = min(a.R, a.tile * a.wr), c = (threadIdx.x % TPR) * 4;
+  const int rr = first + threadIdx.x / TPR, row = rs * a.wr * a.tile + rr;
+  if (rr >= seg_rows || row >= a.R) return;
+  const long long out = static_cast<long long>(bh) * a.R + row;
+  if (parts.n == 0) {
+    *reinterpret_cast<uint2*>(a.o + out * D + c) = make_uint2(0, 0);
+    if (c == 0) a.lse[out] = -INFINITY;
+    return;
+  }
+  float m = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (unsigned k0 = 0; k0 < parts.n; k0 += 4) {
+    float2 ml[4];
+    float4 v[4];
+#pragma unroll
+    for (unsigned k = 0; k < 4; ++k) {
+      ml[k] = make_float2(-INFINITY, 0.f);
+      v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k0 + k < parts.n) {
+        const long long p = parts.index(k0 + k, seg_rows, rr);
+        ml[k] = __ldcg(a.part_ml + p);
+        v[k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + p * D + c));
+      }
+    }
+    const float mn = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), m);
+    const float base = mn == -INFINITY ? 0.f : mn, back = fast_exp2(m - base);
+    m = mn;
+    l *= back;
+    acc.x *= back, acc.y *= back, acc.z *= back, acc.w *= back;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float f = fast_exp2(ml[k].x - base);
+      l = fmaf(ml[k].y, f, l);
+      acc.x = fmaf(v[k].x, f, acc.x), acc.y = fmaf(v[k].y, f, acc.y);
+      acc.z = fmaf(v[k].z, f, acc.z), acc.w = fmaf(v[k].w, f, acc.w);
+    }
+  }
+  store_row<D>(a, out, c, m, l, acc);
+}
+
+template <int D>
+__device__ __forceinline__ void join_one(const CacheAttnArgs& a, const Parts& parts, int bh, int rs,
+                                         int rr) {
   constexpr int TPR = D / 4, PAR = 128 / TPR;
   __shared__ float weight[128];
   __shared__ float4 sum[128];
   __shared__ float s_max[4], s_l[4];
-  grid_dep_wait();
-  const int seg_rows = min(a.R, a.tile * a.wr), rr = blockIdx.y;
-  const int mult = a.Hk * a.row_segs;
-  const int b = blockIdx.x / mult, seg = blockIdx.x - b * mult;
-  const int h = seg / a.row_segs, rs = seg - h * a.row_segs;
-  if (rr >= seg_rows) {
-    if (rs == 0) add_mass(a, ctas, b * a.Hk + h, rr - seg_rows);
-    return;
-  }
+  const int seg_rows = min(a.R, a.tile * a.wr);
   const int c = (threadIdx.x % TPR) * 4, part = threadIdx.x / TPR, warp = warp_id();
   const int row = rs * a.wr * a.tile + rr;
   if (row >= a.R) return;
-  const long long out = (static_cast<long long>(b) * a.Hk + h) * a.R + row;
-  const Parts parts = parts_of(a, b, seg, ctas);
+  const long long out = static_cast<long long>(bh) * a.R + row;
   const unsigned n = parts.n;
   if (n == 0) {
     if (part == 0) *reinterpret_cast<uint2*>(a.o + out * D + c) = make_uint2(0, 0);
     if (threadIdx.x == 0) a.lse[out] = -INFINITY;
+    return;
   }
-  if (n <= 1) return;
+  // the values come with the statistics: up to 128 partials wait for one trip to memory
   float m = -INFINITY;
-  for (unsigned k = threadIdx.x; k < n; k += 128) m = fmaxf(m, a.part_ml[parts.index(k, seg_rows, rr)].x);
+  for (unsigned k = threadIdx.x; k < n; k += 128)
+    m = fmaxf(m, __ldcg(a.part_ml + parts.index(k, seg_rows, rr)).x);
+  constexpr int AHEAD = 8;
+  float4 v[AHEAD];
+#pragma unroll
+  for (unsigned j = 0; j < AHEAD; ++j)
+    if (part + j * PAR < n)
+      v[j] = __ldcg(reinterpret_cast<const float4*>(
+          a.part_o + parts.index(part + j * PAR, seg_rows, rr) * D + c));
   m = warp_max(m);
   if (lane_id() == 0) s_max[warp] = m;
   __syncthreads();
@@ -989,19 +1262,29 @@ __global__ void __launch_bounds__(128) cache_attn_combine_kernel(const CacheAttn
   for (unsigned k0 = 0; k0 < n; k0 += 128) {
     const unsigned k = k0 + threadIdx.x;
     if (k < n) {
-      const float2 ml = a.part_ml[parts.index(k, seg_rows, rr)];
+      const float2 ml = __ldcg(a.part_ml + parts.index(k, seg_rows, rr));
       const float f = fast_exp2(ml.x - base);
       weight[threadIdx.x] = f;
       l = fmaf(ml.y, f, l);
     }
     __syncthreads();
     const unsigned top = min(128u, n - k0);
+    if (k0 == 0) {
+#pragma unroll
+      for (unsigned j = 0; j < AHEAD; ++j)
+        if (part + j * PAR < top) {
+          const float f = weight[part + j * PAR];
+          acc.x = fmaf(v[j].x, f, acc.x), acc.y = fmaf(v[j].y, f, acc.y);
+          acc.z = fmaf(v[j].z, f, acc.z), acc.w = fmaf(v[j].w, f, acc.w);
+        }
+    }
 #pragma unroll 4
-    for (unsigned j = part; j < top; j += PAR) {
+    for (unsigned j = part + (k0 == 0 ? AHEAD * PAR : 0); j < top; j += PAR) {
       const float f = weight[j];
-      const float4 v = *reinterpret_cast<const float4*>(a.part_o + parts.index(k0 + j, seg_rows, rr) * D + c);
-      acc.x = fmaf(v.x, f, acc.x), acc.y = fmaf(v.y, f, acc.y);
-      acc.z = fmaf(v.z, f, acc.z), acc.w = fmaf(v.w, f, acc.w);
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(
+          a.part_o + parts.index(k0 + j, seg_rows, rr) * D + c));
+      acc.x = fmaf(x.x, f, acc.x), acc.y = fmaf(x.y, f, acc.y);
+      acc.z = fmaf(x.z, f, acc.z), acc.w = fmaf(x.w, f, acc.w);
     }
     __syncthreads();
   }
@@ -1012,13 +1295,36 @@ __global__ void __launch_bounds__(128) cache_attn_combine_kernel(const CacheAttn
   if (part != 0) return;
   l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
   for (int p = 1; p < PAR; ++p) {
-    const float4 v = sum[threadIdx.x + p * TPR];
-    acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+    const float4 x = sum[threadIdx.x + p * TPR];
+    acc.x += x.x, acc.y += x.y, acc.z += x.z, acc.w += x.w;
   }
-  const float inv = l > 0.f ? 1.f / l : l;
-  *reinterpret_cast<uint2*>(a.o + out * D + c) =
-      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-  if (c == 0) a.lse[out] = (m + __log2f(l)) * kLn2;
+  store_row<D>(a, out, c, m, l, acc);
+}
+
+// Joins the rows and, with scores, adds the weights up: blockIdx.y is a set of rows of
+// the segment blockIdx.x, a (b, h, row segment), or, from `row_sets` on, a chunk of
+// tokens of the key head (taken by its first row segment).  Where the partials lie
+// follows from the lengths alone, which no kernel writes between the main kernel's start
+// and this one, so that is found before the wait for the main kernel.
+template <int D>
+__global__ void __launch_bounds__(128) cache_attn_combine_kernel(const CacheAttnArgs a,
+                                                                 unsigned ctas, int row_sets) {
+  const int set = blockIdx.y, mult = a.Hk * a.row_segs;
+  const int b = blockIdx.x / mult, seg = blockIdx.x - b * mult;
+  const int h = seg / a.row_segs, rs = seg - h * a.row_segs, bh = b * a.Hk + h;
+  if (set < row_sets) {
+    const Parts parts = parts_of(a, b, seg, ctas);
+    grid_dep_wait();
+    if (parts.n == 1) return;  // one CTA had it whole
+    const int per = join_rows(min(a.R, a.tile * a.wr), D);
+    if (per == 1)
+      join_one<D>(a, parts, bh, rs, set);
+    else
+      join_many<D>(a, parts, bh, rs, set * per);
+    return;
+  }
+  grid_dep_wait();
+  if (rs == 0) add_mass(a, ctas, bh, set - row_sets);
 }
 
 }  // namespace rfb

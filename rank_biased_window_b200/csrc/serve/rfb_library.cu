@@ -107,7 +107,7 @@ CaPlan plan_cache_attn(int B, int Hk, int R, int cap, int d, int r, bool mass, i
   p.ctas = static_cast<int>(most < wave ? (most > 0 ? most : 1) : wave);
   p.ml_bytes = round256(static_cast<size_t>(p.ctas) * 2 * p.seg_rows * sizeof(float2));
   p.o_bytes = round256(static_cast<size_t>(p.ctas) * 2 * p.seg_rows * d * sizeof(float));
-  p.score_bytes = mass ? static_cast<size_t>(B) * Hk * R * cap * sizeof(float) : 0;
+  p.score_bytes = mass && p.tile == 8 ? static_cast<size_t>(B) * Hk * R * cap * sizeof(float) : 0;
   return p;
 }
 
@@ -123,15 +123,19 @@ int launch_cache_attn_main(const CacheAttnArgs& a, const CaPlan& p, cudaStream_t
 
 template <int D, int RP>
 int launch_cache_attn(const CacheAttnArgs& a, const CaPlan& p, cudaStream_t st) {
-  const int rc = p.tile == 8 ? a.scores ? launch_cache_attn_main<D, RP, 1, true>(a, p, st)
-                                        : launch_cache_attn_main<D, RP, 1, false>(a, p, st)
-                 : a.scores  ? launch_cache_attn_main<D, RP, 2, true>(a, p, st)
-                             : launch_cache_attn_main<D, RP, 2, false>(a, p, st);
+  const int rc = p.tile == 16 ? launch_cache_attn_main<D, RP, 2, false>(a, p, st)
+                 : a.scores   ? launch_cache_attn_main<D, RP, 1, true>(a, p, st)
+                              : launch_cache_attn_main<D, RP, 1, false>(a, p, st);
   if (rc != RFB_OK) return rc;
-  const dim3 grid(static_cast<unsigned>(a.B * a.Hk * a.row_segs),
-                  p.seg_rows + (a.scores ? (a.cap + mass_tokens(a.R) - 1) / mass_tokens(a.R) : 0));
-  launch_pdl(cache_attn_combine_kernel<D>, grid, dim3(128), 0, st, a,
-             static_cast<unsigned>(p.ctas));
+  const int per = join_rows(p.seg_rows, D), row_sets = (p.seg_rows + per - 1) / per;
+  const int chunks = a.scores ? (a.cap + mass_tokens(a.R) - 1) / mass_tokens(a.R) : 0;
+  launch_pdl(cache_attn_combine_kernel<D>,
+             dim3(static_cast<unsigned>(a.B * a.Hk * a.row_segs), row_sets + chunks), dim3(128), 0,
+             st, a, static_cast<unsigned>(p.ctas), row_sets);
+  if (a.mass_out && !a.scores)
+    launch_pdl(cache_mass_kernel<D, RP>,
+               dim3(static_cast<unsigned>(a.B * a.Hk), (a.cap + kMassChunk - 1) / kMassChunk),
+               dim3(128), 0, st, a);
   return launch_status();
 }
 
@@ -345,7 +349,7 @@ int rfb_attn_fwd_cache(const void* q, const void* u, const void* k8, const void*
   char* ws = static_cast<char*>(workspace);
   a.part_ml = reinterpret_cast<float2*>(ws);
   a.part_o = reinterpret_cast<float*>(ws + p.ml_bytes);
-  a.scores = mass_out ? reinterpret_cast<float*>(ws + p.ml_bytes + p.o_bytes) : nullptr;
+  a.scores = p.score_bytes ? reinterpret_cast<float*>(ws + p.ml_bytes + p.o_bytes) : nullptr;
   a.mass = mass, a.mass_out = mass_out, a.decay = decay;
   a.B = B, a.Hk = heads_kv, a.R = static_cast<int>(R), a.Nq = Nq, a.cap = cap, a.r = r;
   a.tile = p.tile, a.wr = p.wr, a.row_segs = p.row_segs;

@@ -128,12 +128,12 @@ def attention(q, u, k, v, w, lengths, scale, causal, mass=None, decay=1.0):
             # a score in fp32: at most 12 accumulation steps and the two scalings, 2^-18 of the
             # sum of magnitudes; so a probability is off by twice that, by the exponential's
             # 2^-21 and by its rounding to fp16: half a step is 2^-11 of a normal value and 2^-25
-            # below 2^-14; the kernel's weights are lifted by 2^15, so the latter is 2^-40 of the
-            # largest weight (which matters where a small weight meets a large value)
+            # below 2^-14; the kernel's weights are lifted by 2^11 at least, so the latter is 2^-36
+            # of the largest weight (which matters where a small weight meets a large value)
             off = (torch.nan_to_num(size) * seen).amax(-1) * 2.0 ** -18
             a = pv.abs().sum(1)
             room_o[b, h] = (2.0 ** -11 + 2.0 ** -19 + 4 * off[:, None]) * a + 2.0 ** -8 * o[b, h].abs() \
-                + 2.0 ** -40 * p.amax(-1)[:, None] * torch.nan_to_num(seen[..., None] * vv.abs()[None]).sum(1)
+                + 2.0 ** -36 * p.amax(-1)[:, None] * torch.nan_to_num(seen[..., None] * vv.abs()[None]).sum(1)
             room_lse[b, h] = 2 * off + 2.0 ** -20 + torch.nan_to_num(top.abs(), posinf=0.0) * 2.0 ** -22
             if mass is not None:
                 new_mass[b, hk, :L] += p.sum(0)
