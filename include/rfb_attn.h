@@ -313,7 +313,7 @@ RFB_API int rfb_bias_project(const float* bias, const float* x, float* out, int 
  * rot even, 0 <= rot <= d <= 1024.  Pointers need the alignment of their
  * elements; with 16-byte aligned pointers, strides of whole 16-byte units, d a
  * multiple of 16 bytes and rot / 2 (layout 0) or rot (layout 1) as well, the
- * copies are 16 bytes wide.  Sequences B <= 65535.
+ * copies are 16 bytes wide.  B <= 65535, N * d < 2^32 - 128.
  */
 RFB_API int rfb_rotary(const void* q, const void* k, void* q_out, void* k_out,
                        const int* positions, const double* freqs, int B, int heads, int heads_kv,

@@ -13,7 +13,7 @@
 
 namespace rfb {
 
-constexpr int kAppendWarps = 4;
+constexpr int kAppendWarps = 8;
 
 struct AppendArgs {
   const __nv_bfloat16* x[3];      // new k, v, w

@@ -23,7 +23,7 @@ constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelMaxKeys = 32;  // keys a thread of cache_select_kernel holds
 constexpr int kMoveWarps = 8;
-constexpr int kMoveStages = 3;
+constexpr int kMoveStages = 2;
 
 struct EvictArgs {
   const uint8_t* codes[3];

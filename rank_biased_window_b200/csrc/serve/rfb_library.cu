@@ -46,7 +46,8 @@ int launch_rotary(RotArgs& a, int B, int sms, cudaStream_t st) {
   const long long blocks =
       (static_cast<long long>(a.N) * a.units + kRotThreads - 1) / kRotThreads;
   const int groups = (heads + per - 1) / per;
-  if (blocks > 0x7fffffffLL || B > 65535 || groups > 65535) return RFB_ERR_UNSUPPORTED;
+  if (blocks * kRotThreads > 0xffffffffLL || B > 65535 || groups > 65535)
+    return RFB_ERR_UNSUPPORTED;
   const dim3 grid(static_cast<unsigned>(blocks), groups, B);
   launch_pdl(rotary_kernel<T, HALF, VEC>, grid, dim3(kRotThreads), 0, st, a);
   return launch_status();

@@ -110,10 +110,10 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotArgs a) {
   constexpr int V = R::VEC;
   constexpr int PAIRS = !VEC_OK ? 1 : HALF ? V : V / 2;
   grid_dep_wait();
-  const long long idx = static_cast<long long>(blockIdx.x) * kRotThreads + threadIdx.x;
-  const int n = static_cast<int>(idx / a.units);
-  if (n >= a.N) return;
-  const int unit = static_cast<int>(idx - static_cast<long long>(n) * a.units);
+  const unsigned idx = blockIdx.x * kRotThreads + threadIdx.x;  // N * units < 2^32
+  const unsigned n = idx / static_cast<unsigned>(a.units);
+  if (n >= static_cast<unsigned>(a.N)) return;
+  const int unit = static_cast<int>(idx - n * a.units);
   const int b = blockIdx.z;
   const int turning = a.rot / (2 * PAIRS);  // units that rotate
   const bool copy = unit >= turning;
@@ -127,67 +127,65 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotArgs a) {
 #pragma unroll
     for (int i = 0; i < PAIRS; ++i) rot_angle(a, pos, unit * PAIRS + i, cs[i], sn[i]);
   }
-  const int total = a.heads[0] + a.heads[1];
-  const int h0 = blockIdx.y * a.heads_per_thread;
-  const int h1 = min(h0 + a.heads_per_thread, total);
-  const auto in = [&](int hh) {
-    const int z = hh >= a.heads[0], h = z ? hh - a.heads[0] : hh;
-    return static_cast<const T*>(a.x[z]) + b * a.sb[z] + h * a.sh[z] + n * a.sn[z];
-  };
-  const auto out = [&](int hh) {
-    const int z = hh >= a.heads[0], h = z ? hh - a.heads[0] : hh;
-    return static_cast<T*>(a.y[z]) + ((static_cast<long long>(b) * a.heads[z] + h) * a.N + n) * a.d;
-  };
-  if constexpr (VEC_OK) {
-    // the loads of BATCH heads go out before the first of their stores
-    constexpr int BATCH = HALF ? 2 : 4;
-    for (int hh = h0; hh < h1; hh += BATCH) {
-      uint4 v0[BATCH], v1[BATCH];
+  const int h0 = blockIdx.y * a.heads_per_thread, h1 = h0 + a.heads_per_thread;
+#pragma unroll 1
+  for (int z = 0; z < 2; ++z) {  // the group's heads of q, then of k
+    const int skip = z ? a.heads[0] : 0;
+    const int from = max(h0 - skip, 0), to = min(h1 - skip, a.heads[z]);
+    if (from >= to) continue;
+    const T* x = static_cast<const T*>(a.x[z]) + b * a.sb[z] + from * a.sh[z] + n * a.sn[z];
+    T* y = static_cast<T*>(a.y[z]) +
+           ((static_cast<long long>(b) * a.heads[z] + from) * a.N + n) * a.d;
+    const long long in_step = a.sh[z], out_step = static_cast<long long>(a.N) * a.d;
+    if constexpr (VEC_OK) {
+      // the loads of BATCH heads go out before the first of their stores
+      constexpr int BATCH = HALF ? 2 : 4;
+      for (int h = from; h < to; h += BATCH, x += BATCH * in_step, y += BATCH * out_step) {
+        uint4 v0[BATCH], v1[BATCH];
 #pragma unroll
-      for (int k = 0; k < BATCH; ++k) {
-        if (hh + k >= h1) break;
-        v0[k] = __ldcs(reinterpret_cast<const uint4*>(in(hh + k) + c0));
-        if (HALF && !copy) v1[k] = __ldcs(reinterpret_cast<const uint4*>(in(hh + k) + c1));
-      }
+        for (int k = 0; k < BATCH; ++k) {
+          if (h + k >= to) break;
+          v0[k] = __ldcs(reinterpret_cast<const uint4*>(x + k * in_step + c0));
+          if (HALF && !copy) v1[k] = __ldcs(reinterpret_cast<const uint4*>(x + k * in_step + c1));
+        }
 #pragma unroll
-      for (int k = 0; k < BATCH; ++k) {
-        if (hh + k >= h1) break;
-        T* y = out(hh + k);
-        if (copy) {
-          *reinterpret_cast<uint4*>(y + c0) = v0[k];
-        } else if constexpr (HALF) {
-          float p[V], q[V], o0[V], o1[V];
-          R::load(v0[k], p);
-          R::load(v1[k], q);
+        for (int k = 0; k < BATCH; ++k) {
+          if (h + k >= to) break;
+          T* yk = y + k * out_step;
+          if (copy) {
+            *reinterpret_cast<uint4*>(yk + c0) = v0[k];
+          } else if constexpr (HALF) {
+            float p[V], q[V], o0[V], o1[V];
+            R::load(v0[k], p);
+            R::load(v1[k], q);
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            o0[i] = p[i] * cs[i] - q[i] * sn[i];
-            o1[i] = q[i] * cs[i] + p[i] * sn[i];
+            for (int i = 0; i < V; ++i) {
+              o0[i] = p[i] * cs[i] - q[i] * sn[i];
+              o1[i] = q[i] * cs[i] + p[i] * sn[i];
+            }
+            *reinterpret_cast<uint4*>(yk + c0) = R::store(o0);
+            *reinterpret_cast<uint4*>(yk + c1) = R::store(o1);
+          } else {
+            float p[V], o[V];
+            R::load(v0[k], p);
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+              o[2 * i] = p[2 * i] * cs[i] - p[2 * i + 1] * sn[i];
+              o[2 * i + 1] = p[2 * i + 1] * cs[i] + p[2 * i] * sn[i];
+            }
+            *reinterpret_cast<uint4*>(yk + c0) = R::store(o);
           }
-          *reinterpret_cast<uint4*>(y + c0) = R::store(o0);
-          *reinterpret_cast<uint4*>(y + c1) = R::store(o1);
-        } else {
-          float p[V], o[V];
-          R::load(v0[k], p);
-#pragma unroll
-          for (int i = 0; i < V / 2; ++i) {
-            o[2 * i] = p[2 * i] * cs[i] - p[2 * i + 1] * sn[i];
-            o[2 * i + 1] = p[2 * i + 1] * cs[i] + p[2 * i] * sn[i];
-          }
-          *reinterpret_cast<uint4*>(y + c0) = R::store(o);
         }
       }
-    }
-  } else {
-    for (int hh = h0; hh < h1; ++hh) {
-      const T* x = in(hh);
-      T* y = out(hh);
-      if (copy) {
-        y[c0] = x[c0];
-      } else {
-        const float p = R::one(x[c0]), q = R::one(x[c1]);
-        y[c0] = R::to(p * cs[0] - q * sn[0]);
-        y[c1] = R::to(q * cs[0] + p * sn[0]);
+    } else {
+      for (int h = from; h < to; ++h, x += in_step, y += out_step) {
+        if (copy) {
+          y[c0] = x[c0];
+        } else {
+          const float p = R::one(x[c0]), q = R::one(x[c1]);
+          y[c0] = R::to(p * cs[0] - q * sn[0]);
+          y[c1] = R::to(q * cs[0] + p * sn[0]);
+        }
       }
     }
   }
