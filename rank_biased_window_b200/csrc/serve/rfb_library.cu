@@ -133,7 +133,7 @@ int launch_cache_attn(const CacheAttnArgs& a, const CaPlan& p, cudaStream_t st) 
   launch_pdl(cache_attn_combine_kernel<D>,
              dim3(static_cast<unsigned>(a.B * a.Hk * a.row_segs), row_sets + chunks), dim3(128), 0,
              st, a, static_cast<unsigned>(p.ctas), row_sets);
-  if (a.mass_out && !a.scores)
+  if (a.mass_out && !a.scores && a.cap > 0)
     launch_pdl(cache_mass_kernel<D, RP>,
                dim3(static_cast<unsigned>(a.B * a.Hk), (a.cap + kMassChunk - 1) / kMassChunk),
                dim3(128), 0, st, a);

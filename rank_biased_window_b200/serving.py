@@ -46,15 +46,17 @@ def _cuda(name, t):
     return t.device
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
 def _launch(device, stream, call, *args):
     """call(*args, stream pointer) with the device and the stream current, so
     that what the call allocates belongs to the stream it runs on.  The usual
     case, the current stream of the current device, changes neither."""
-    if stream is None and device.index == torch.cuda.current_device():
-        return call(*args, _raw_stream(device.index))
+    if stream is None:
+        index = device.index
+        if index == _current_device():
+            return call(*args, _raw_stream(index))
     with _on_device(device):
         if stream is None:
             return call(*args, _raw_stream(device.index))
@@ -64,6 +66,13 @@ def _launch(device, stream, call, *args):
 
 def _p(t):
     return None if t is None else t.data_ptr()
+
+
+def _empty_like(t):
+    """A contiguous tensor of t's shape and type."""
+    if t.is_contiguous():
+        return torch.empty_like(t)
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 _Strides6, _Strides9 = ctypes.c_longlong * 6, ctypes.c_longlong * 9
@@ -143,13 +152,13 @@ def _rotary(q, k, positions, freqs, layout, amplitude, inverse, q_out, k_out, st
     own_rows = positions.dim() == 2
     _require("positions", positions, torch.int32, (B, N) if own_rows else (N,), dev)
     if q_out is None:
-        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        q_out = _empty_like(q)
     else:
         _require("q_out", q_out, dtype, shape, dev)
     if k is None:
         k_out = None
     elif k_out is None:
-        k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+        k_out = _empty_like(k)
     else:
         _require("k_out", k_out, dtype, k.shape, dev)
     strides = _Strides6(sq[0], sq[1], sq[2], sk[0], sk[1], sk[2])
@@ -185,23 +194,25 @@ def rotary_bwd(dq, dk, positions, freqs, *, layout="half", amplitude=1.0, q_out=
 
 
 class RFBRotary(torch.autograd.Function):
-    """Autograd wrapper of rotary_fwd / rotary_bwd."""
+    """Autograd wrapper of rotary_fwd / rotary_bwd.  The rotation is linear and its
+    gradient the inverse one, so the backward is this function again."""
 
     @staticmethod
-    def forward(ctx, q, k, positions, freqs, layout, amplitude):
+    def forward(ctx, q, k, positions, freqs, layout, amplitude, inverse=False):
         ctx.save_for_backward(positions, freqs)
-        ctx.layout, ctx.amplitude = layout, amplitude
-        return rotary_fwd(q, k, positions, freqs, layout=layout, amplitude=amplitude)
+        ctx.layout, ctx.amplitude, ctx.inverse = layout, amplitude, inverse
+        turn = rotary_bwd if inverse else rotary_fwd
+        return turn(q, k, positions, freqs, layout=layout, amplitude=amplitude)
 
     @staticmethod
     def backward(ctx, dq, dk):
         positions, freqs = ctx.saved_tensors
 
         def rows(t):
-            return t if t.stride(3) == 1 or t.shape[3] == 1 else t.contiguous()
-        gq, gk = rotary_bwd(rows(dq), None if dk is None else rows(dk), positions, freqs,
-                            layout=ctx.layout, amplitude=ctx.amplitude)
-        return gq, gk, None, None, None, None
+            return t if t is None or t.stride(3) == 1 or t.shape[3] == 1 else t.contiguous()
+        gq, gk = RFBRotary.apply(rows(dq), rows(dk), positions, freqs, ctx.layout, ctx.amplitude,
+                                 not ctx.inverse)
+        return gq, gk, None, None, None, None, None
 
 
 def rfb_rotary(q, k, positions, freqs, layout="half", amplitude=1.0):

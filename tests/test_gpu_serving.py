@@ -107,6 +107,23 @@ def test_rotary_gradient(rfb_lib, cuda_dev, layout):
     assert torch.equal(a, b)
 
 
+def test_rotary_single_tensor_and_second_order(rfb_lib, cuda_dev):
+    """k None, one output unused, and a gradient of a gradient (the rotation
+    is linear: it is the rotation of what the gradient is multiplied with)."""
+    g = gen(13)
+    q, w = (torch.randn(1, 2, 3, 16, generator=g).to(cuda_dev).requires_grad_() for _ in range(2))
+    pos, (f, _) = ints([4, 0, 9], cuda_dev), rfb_lib.rotary_frequencies(16, device=cuda_dev)
+    y, none = rfb_lib.rfb_rotary(q, None, pos, f)
+    assert none is None
+    gq, = torch.autograd.grad(y, q, w, create_graph=True)
+    z = torch.randn(1, 2, 3, 16, generator=g).to(cuda_dev)
+    gw, = torch.autograd.grad(gq, w, z)
+    assert torch.equal(gw, rfb_lib.rotary_fwd(z, None, pos, f)[0])
+    a, b = rfb_lib.rfb_rotary(q, w, pos, f)
+    ga, gb = torch.autograd.grad(b, (q, w), z)
+    assert bool((ga == 0).all()) and torch.equal(gb, rfb_lib.rotary_bwd(z, None, pos, f)[0])
+
+
 def test_rotary_before_attention_trains(rfb_lib, cuda_dev):
     """rfb_rotary feeds rfb_attention: the gradients reach the unrotated
     operands and are the inverse turn of the attention's own."""
@@ -547,6 +564,116 @@ def test_captured_rotary_backward(rfb_lib, cuda_dev):
         got = rfb_lib.rotary_bwd(q, None, p, f)[0]
     graph.replay()
     assert torch.equal(got, want)
+
+
+def test_empty_cache_and_empty_calls(rfb_lib, cuda_dev):
+    """A cache without capacity, calls without sequences, rows or tokens."""
+    for rows in (1, 3):
+        c = rfb_lib.Cache8.create(2, 2, 0, 64, 8, mass=True, device=cuda_dev)
+        q = torch.randn(2, 8, rows, 64, device=cuda_dev).bfloat16()
+        u = torch.randn(2, 8, rows, 8, device=cuda_dev).bfloat16()
+        o, lse = rfb_lib.attn_fwd_cache(q, u, c, ints([0, 5], cuda_dev), mass_out=c.mass)
+        assert bool((o == 0).all()) and bool((lse == float("-inf")).all())
+        x = torch.randn(2, 2, 1, 64, device=cuda_dev).bfloat16()
+        rfb_lib.cache_append(c, x, x, x[..., :8].contiguous(), start=ints([0, 0], cuda_dev))
+    c, _ = filled(rfb_lib, cuda_dev, 2, 2, 64, 64, 0, seed=3)
+    before = c.k.view(torch.uint8).clone()
+    x = torch.randn(2, 2, 0, 64, device=cuda_dev).bfloat16()
+    rfb_lib.cache_append(c, x, x, start=ints([3, 3], cuda_dev))
+    o, lse = rfb_lib.attn_fwd_cache(torch.zeros(2, 4, 0, 64, device=cuda_dev).bfloat16(), None, c,
+                                    ints([3, 3], cuda_dev))
+    assert o.shape == (2, 4, 0, 64) and lse.shape == (2, 4, 0)
+    assert torch.equal(c.k.view(torch.uint8), before)
+    e = rfb_lib.Cache8.create(0, 2, 64, 64, mass=True, device=cuda_dev)
+    n, kept = rfb_lib.cache_evict(e, ints([], cuda_dev), 5)
+    assert n.shape == (0,) and kept.shape == (0, 2, 5)
+
+
+def test_offsets_past_32_bits(rfb_lib, cuda_dev):
+    """The last sequence of a cache of more than 2^32 bytes a tensor."""
+    B, cap, d = 66, 524288, 128
+    assert (B - 1) * cap * d > 2 ** 32
+    cache = rfb_lib.Cache8.create(B, 1, cap, d, mass=True, device=cuda_dev)
+    small = rfb_lib.Cache8.create(1, 1, 4096, d, mass=True, device=cuda_dev)
+    g = gen(151)
+    k, v = (torch.randn(1, 1, 3000, d, generator=g).bfloat16().to(cuda_dev) for _ in range(2))
+    q = torch.randn(1, 3, 1, d, generator=g).bfloat16().to(cuda_dev)
+    rfb_lib.cache_append(small, k, v, start=ints([0], cuda_dev))
+    o, lse = rfb_lib.attn_fwd_cache(q, None, small, ints([3000], cuda_dev), mass_out=small.mass)
+    counts = ints([0] * (B - 1) + [3000], cuda_dev)
+    zero = torch.zeros(B, dtype=torch.int32, device=cuda_dev)
+    rfb_lib.cache_append(cache, k.expand(B, 1, 3000, d), v.expand(B, 1, 3000, d), start=zero,
+                         counts=counts)
+    ob, lb = rfb_lib.attn_fwd_cache(q.expand(B, 3, 1, d).contiguous(), None, cache, counts,
+                                    mass_out=cache.mass)
+    assert bool((ob[:-1] == 0).all()) and bool((lb[:-1] == float("-inf")).all())
+    # the work is cut elsewhere: O a bf16 step apart at most, LSE and mass a few fp32 steps
+    assert float((ob[-1].double() - o[0].double()).abs().max()) <= 2.0 ** -7 * float(o.abs().max())
+    assert torch.allclose(lb[-1], lse[0], rtol=2.0 ** -21, atol=2.0 ** -20)
+    assert torch.allclose(cache.mass[-1], small.mass[0, :, :1].new_zeros(1, cap).index_copy(
+        1, torch.arange(3000, device=cuda_dev), small.mass[0, :, :3000]), rtol=2.0 ** -17, atol=2.0 ** -30)
+    cache.mass[-1, 0, :3000] = small.mass[0, 0, :3000]  # the same bits, so the same choice
+    n, kept = rfb_lib.cache_evict(cache, counts, 1000, 100)
+    ns, ks = rfb_lib.cache_evict(small, ints([3000], cuda_dev), 1000, 100)
+    assert n.tolist() == [0] * (B - 1) + [1000] and torch.equal(kept[-1], ks[0])
+    assert torch.equal(cache.k[-1, :, :1000].view(torch.uint8), small.k[0, :, :1000].view(torch.uint8))
+    assert torch.equal(cache.v[-1, :, :1000].view(torch.uint8), small.v[0, :, :1000].view(torch.uint8))
+
+
+@pytest.mark.parametrize("Nq,sites", [(1, (71,)), (20, (70, 71)), (70, (70, 71))])
+def test_waits_that_give_up(rfb_lib, cuda_dev, Nq, sites):
+    """A wait of the attention's copy pipeline that gives up at once: the error
+    word names its site, the call ends, and the next one is right.  Then a limit
+    of 1 us, under which a call ends either way."""
+    cache, refs = filled(rfb_lib, cuda_dev, 3, 2, 2048, 64, 8, seed=161)
+    lengths = [2000, 1999, 700]
+    want = run_attn(rfb_lib, cuda_dev, cache, refs, lengths, 4, Nq, seed=7)
+    torch.cuda.synchronize()
+    assert rfb_lib.last_device_error() == 0
+    for limit, site in [(0, s) for s in sites] + [(1, -1)]:
+        try:
+            rfb_lib.debug_set_wait_limit(limit, site)
+            q = torch.randn(3, 4, Nq, 64, generator=gen(8)).bfloat16().to(cuda_dev)
+            u = torch.randn(3, 4, Nq, 8, generator=gen(9)).bfloat16().to(cuda_dev)
+            rfb_lib.attn_fwd_cache(q, u, cache, ints(lengths, cuda_dev))
+            err = rfb_lib.last_device_error()
+        finally:
+            rfb_lib.debug_set_wait_limit(0, -1)
+        assert err == (6 | site << 8) if site >= 0 else err & 0xff in (0, 6)
+        again = run_attn(rfb_lib, cuda_dev, cache, refs, lengths, 4, Nq, seed=7)
+        assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+        assert rfb_lib.last_device_error() == 0
+
+
+def test_nothing_outside_the_outputs(rfb_lib, cuda_dev):
+    """Every output between canaries that no kernel writes."""
+    def guarded(shape, dtype):
+        n = math.prod(shape)
+        raw = torch.full((n + 8192,), 77.0, dtype=dtype, device=cuda_dev) if dtype != torch.uint8 else \
+            torch.full((n + 8192,), 77, dtype=dtype, device=cuda_dev)
+        return raw, raw[4096:4096 + n].view(shape)
+
+    def intact(raw):
+        return bool((raw[:4096] == 77).all()) and bool((raw[-4096:] == 77).all())
+    for d, r, H, Hk, Nq in [(64, 24, 6, 2, 1), (32, 8, 5, 1, 7), (128, 0, 4, 4, 1), (64, 64, 8, 1, 9)]:
+        lengths = [97, 1, 160, 0]
+        cache, refs = filled(rfb_lib, cuda_dev, 4, Hk, 160, d, r, seed=171, mass=True)
+        q = torch.randn(4, H, Nq, d, generator=gen(172)).bfloat16().to(cuda_dev)
+        u = torch.randn(4, H, Nq, r, generator=gen(173)).bfloat16().to(cuda_dev) if r else None
+        ro, out = guarded((4, H, Nq, d), torch.bfloat16)
+        rl, lse = guarded((4, H, Nq), torch.float32)
+        rm, mass = guarded((4, Hk, 160), torch.float32)
+        rw, ws = guarded((rfb_lib.attn_cache_workspace_size(cache, H, Nq, True),), torch.uint8)
+        L = ints(lengths, cuda_dev)
+        rfb_lib.attn_fwd_cache(q, u, cache, L, mass=cache.mass, mass_out=mass, out=out, lse=lse,
+                               workspace=ws)
+        o, l = rfb_lib.attn_fwd_cache(q, u, cache, L)
+        assert all(intact(x) for x in (ro, rl, rm, rw))
+        assert torch.equal(o, out) and torch.equal(l, lse)
+        rq, qo = guarded((4, H, Nq, d), torch.bfloat16)
+        f, _ = rfb_lib.rotary_frequencies(d // 2 - 2, device=cuda_dev)
+        rfb_lib.rotary_fwd(q, None, ints(list(range(Nq)), cuda_dev), f, q_out=qo)
+        assert intact(rq)
 
 
 def test_other_stream(rfb_lib, cuda_dev):
