@@ -1,11 +1,13 @@
-"""Builds the in-tree CUDA library ``librfb_attn.so`` for sm_100a with nvcc.
+"""Builds the in-tree CUDA library ``librfb_attn.so`` for sm_100a with nvcc, and
+the serving calls' Python extension ``_serving_bind.so`` with the host compiler.
 
     python -m rank_biased_window_b200.build [--verbose-ptxas] [--force]
 
 The library is a plain C-ABI shared object (see include/rfb_attn.h); the
 Python binding loads it with ctypes.  The CUDA runtime is linked statically and
 the driver's tensor-map encoder is fetched at run time, so the .so depends on
-nothing but the NVIDIA driver.
+nothing but the NVIDIA driver.  The extension holds host code only and belongs
+to the Python and torch that it was built with.
 """
 from __future__ import annotations
 
@@ -15,12 +17,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "librfb_attn.so")
+BIND = os.path.join(PKG, "_serving_bind.so")
+BIND_SOURCE = os.path.join(CSRC, "serve", "bind.cpp")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -37,14 +42,42 @@ def sources():
                   + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+def _newer(target, inputs) -> bool:
+    if not os.path.exists(target):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(s) <= t for s in sources())
+    t = os.path.getmtime(target)
+    return all(os.path.getmtime(s) <= t for s in inputs)
+
+
+def up_to_date() -> bool:
+    return _newer(LIB, sources())
+
+
+def build_bind(force: bool = False) -> str:
+    if not force and _newer(BIND, [BIND_SOURCE, *glob.glob(os.path.join(INCLUDE, "*.h"))]):
+        return BIND
+    import torch
+    where = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    tmp = BIND + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC",
+           "-fvisibility=hidden", f'-DRFB_TORCH_VERSION="{torch.__version__}"',
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE,
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(where, "include"),
+           "-isystem", os.path.join(where, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), "-L", os.path.join(where, "lib"),
+           "-o", tmp, BIND_SOURCE,
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        sys.stderr.write(res.stdout + res.stderr)
+        raise RuntimeError("building _serving_bind.so failed")
+    os.replace(tmp, BIND)
+    return BIND
 
 
 def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = True) -> str:
+    build_bind(force)
     if not force and up_to_date():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"

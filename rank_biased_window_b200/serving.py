@@ -2,10 +2,14 @@
 rank-factorised bias, eviction): the Python side of the serving entry points in
 include/rfb_attn.h.
 
-Argument marshalling only, as in binding.py.  Tensors that a call makes
-(outputs, workspace) are allocated on the stream that it runs on.  Every call
-may be captured into a CUDA graph; lengths and positions are read on the
-device, so a replayed step follows them.
+Tensors that a call makes (outputs, workspace) are allocated on the stream
+that it runs on.  Every call may be captured into a CUDA graph; lengths and
+positions are read on the device, so a replayed step follows them.
+
+The tensors are checked, made and handed to the C entry points by the
+extension _serving_bind (csrc/serve/bind.cpp): a decode step makes thousands of
+such calls a second, and marshalling them here, as binding.py does for the long
+calls, took two to three times as long as the calls themselves.
 """
 from __future__ import annotations
 
@@ -14,12 +18,32 @@ import math
 
 import torch
 
-from .binding import RFB_ERR_WORKSPACE, _check, _on_device, load_library
+from .binding import _on_device, load_library
 
 CACHE_BLOCK = 32  # tokens per scale
 E4M3 = torch.float8_e4m3fn
 _LAYOUTS = {"half": 0, "interleaved": 1}
-_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+_bind = None
+
+
+def _load_bind():
+    """The extension, given the addresses of the library's functions."""
+    global _bind
+    lib = load_library()
+    try:
+        from . import _serving_bind
+    except ImportError as e:
+        raise RuntimeError("the serving extension is not built for this Python and torch "
+                           "(run `python -m rank_biased_window_b200.build --force`)") from e
+    if _serving_bind.torch_version != torch.__version__:
+        raise RuntimeError(f"the serving extension was built for torch {_serving_bind.torch_version} "
+                           "(run `python -m rank_biased_window_b200.build --force`)")
+    names = ("rfb_rotary", "rfb_cache_append", "rfb_attn_fwd_cache_workspace_size",
+             "rfb_attn_fwd_cache", "rfb_cache_evict", "rfb_strerror", "rfb_last_cuda_error")
+    _serving_bind.init(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names))
+    _bind = _serving_bind
+    return _bind
 
 
 def _require(name, t, dtype, shape, device, contiguous=True):
@@ -46,36 +70,13 @@ def _cuda(name, t):
     return t.device
 
 
-_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-
-
-def _launch(device, stream, call, *args):
-    """call(*args, stream pointer) with the device and the stream current, so
-    that what the call allocates belongs to the stream it runs on.  The usual
-    case, the current stream of the current device, changes neither."""
-    if stream is None:
-        index = device.index
-        if index == _current_device():
-            return call(*args, _raw_stream(index))
-    with _on_device(device):
-        if stream is None:
-            return call(*args, _raw_stream(device.index))
-        with torch.cuda.stream(stream):
-            return call(*args, stream.cuda_stream)
-
-
-def _p(t):
-    return None if t is None else t.data_ptr()
-
-
-def _empty_like(t):
-    """A contiguous tensor of t's shape and type."""
-    if t.is_contiguous():
-        return torch.empty_like(t)
-    return torch.empty_like(t, memory_format=torch.contiguous_format)
-
-
-_Strides6, _Strides9 = ctypes.c_longlong * 6, ctypes.c_longlong * 9
+def _on_stream(device, stream, call, *args):
+    """call(*args) with the caller's stream current, so that what it allocates
+    belongs to the stream it runs on."""
+    if stream.device != device:
+        raise ValueError(f"stream belongs to {stream.device}, the tensors to {device}")
+    with torch.cuda.stream(stream):
+        return call(*args)
 
 
 # ------------------------------------------------------------------- rotary
@@ -124,52 +125,17 @@ def rotary_frequencies(rot, base=10000.0, *, scaling="none", factor=1.0, origina
     return freqs.to(device) if device is not None else freqs, amplitude
 
 
-def _rotary(q, k, positions, freqs, layout, amplitude, inverse, q_out, k_out, st):
-    dev, dtype, shape = q.device, q.dtype, q.shape
+def _rotary(q, k, positions, freqs, layout, amplitude, inverse, q_out, k_out, stream):
+    bind = _bind
+    if bind is None:
+        _cuda("q", q)
+        bind = _load_bind()
     if layout not in _LAYOUTS:
         raise ValueError("layout must be 'half' or 'interleaved'")
-    if dtype not in _DTYPES:
-        raise TypeError(f"q must be bfloat16, float16 or float32, got {dtype}")
-    if len(shape) != 4:
-        raise ValueError("q must be [B, H, N, d]")
-    B, H, N, d = shape
-    sq, Hk, sk = q.stride(), 0, (0, 0, 0, 1)
-    if k is not None:
-        if not isinstance(k, torch.Tensor) or k.dim() != 4:
-            raise ValueError("k must be [B, H, N, d]")
-        Hk, sk = k.shape[1], k.stride()
-        _require("k", k, dtype, (B, Hk, N, d), dev, False)
-    if d > 1 and (sq[3] != 1 or sk[3] != 1):
-        raise ValueError(f"{'q' if sq[3] != 1 else 'k'} must have contiguous channels")
-    if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1:
-        raise ValueError("freqs must be [rot / 2]")
-    pairs = freqs.shape[0]
-    _require("freqs", freqs, torch.float64, (pairs,), dev)
-    if 2 * pairs > d:
-        raise ValueError(f"freqs has {pairs} pairs, more than half of d = {d}")
-    if not isinstance(positions, torch.Tensor) or positions.dim() not in (1, 2):
-        raise ValueError("positions must be [N] or [B, N]")
-    own_rows = positions.dim() == 2
-    _require("positions", positions, torch.int32, (B, N) if own_rows else (N,), dev)
-    if q_out is None:
-        q_out = _empty_like(q)
-    else:
-        _require("q_out", q_out, dtype, shape, dev)
-    if k is None:
-        k_out = None
-    elif k_out is None:
-        k_out = _empty_like(k)
-    else:
-        _require("k_out", k_out, dtype, k.shape, dev)
-    strides = _Strides6(sq[0], sq[1], sq[2], sk[0], sk[1], sk[2])
-    at = ctypes.addressof(strides)
-    rc = load_library().rfb_rotary(
-        q.data_ptr(), _p(k), q_out.data_ptr(), _p(k_out), positions.data_ptr(), freqs.data_ptr(),
-        B, H, Hk, N, d, 2 * pairs, at, at + 24, N if own_rows else 0, _LAYOUTS[layout],
-        _DTYPES[dtype], amplitude, inverse, st)
-    if rc:
-        _check(rc, "rfb_rotary")
-    return q_out, k_out
+    args = (q, k, positions, freqs, _LAYOUTS[layout], amplitude, inverse, q_out, k_out)
+    if stream is None:
+        return bind.rotary(*args)
+    return _on_stream(_cuda("q", q), stream, bind.rotary, *args)
 
 
 def rotary_fwd(q, k, positions, freqs, *, layout="half", amplitude=1.0, q_out=None, k_out=None,
@@ -182,15 +148,13 @@ def rotary_fwd(q, k, positions, freqs, *, layout="half", amplitude=1.0, q_out=No
     layout that attention takes.  positions: int32 [N] or [B, N]; freqs: fp64
     [rot / 2] from rotary_frequencies (channels from rot on pass through).
     """
-    return _launch(_cuda("q", q), stream, _rotary, q, k, positions, freqs, layout, amplitude, 0,
-                   q_out, k_out)
+    return _rotary(q, k, positions, freqs, layout, amplitude, 0, q_out, k_out, stream)
 
 
 def rotary_bwd(dq, dk, positions, freqs, *, layout="half", amplitude=1.0, q_out=None, k_out=None,
                stream=None):
     """Gradients of q and k from those of rotary_fwd's outputs (the inverse turn)."""
-    return _launch(_cuda("dq", dq), stream, _rotary, dq, dk, positions, freqs, layout, amplitude, 1,
-                   q_out, k_out)
+    return _rotary(dq, dk, positions, freqs, layout, amplitude, 1, q_out, k_out, stream)
 
 
 class RFBRotary(torch.autograd.Function):
@@ -227,13 +191,12 @@ class Cache8:
     k, v: e4m3 [B, Hk, cap, d]; w: e4m3 [B, Hk, cap, r] or None; k_scale,
     v_scale, w_scale: fp32 [B, Hk, cap / 32], one power of two per head and 32
     tokens; mass: fp32 [B, Hk, cap], the attention weight that each token
-    gathered, or None.  The object holds the tensors and their addresses; how
-    many tokens a sequence has is the caller's (int32 [B] on the device), one
+    gathered, or None.  The object holds the tensors; how many tokens a sequence has is the caller's (int32 [B] on the device), one
     for all layers of a model.
     """
 
     __slots__ = ("k", "v", "w", "k_scale", "v_scale", "w_scale", "mass", "device", "B", "Hk", "cap",
-                 "d", "r", "_ptrs", "_workspace_bytes")
+                 "d", "r", "_tensors")
 
     def __init__(self, k, v, w, k_scale, v_scale, w_scale, mass=None):
         dev = _cuda("k", k)
@@ -261,8 +224,10 @@ class Cache8:
         self.k_scale, self.v_scale, self.w_scale = k_scale, v_scale, w_scale
         self.mass, self.device = mass, dev
         self.B, self.Hk, self.cap, self.d, self.r = B, Hk, cap, d, r
-        self._ptrs = tuple(_p(t) for t in (k, v, w, k_scale, v_scale, w_scale))
-        self._workspace_bytes = {}  # by (heads, Nq, with mass)
+        self._tensors = (_bind or _load_bind()).cache(k, v, w, k_scale, v_scale, w_scale)
+
+    def __reduce__(self):  # copy and pickle
+        return Cache8, (self.k, self.v, self.w, self.k_scale, self.v_scale, self.w_scale, self.mass)
 
     @classmethod
     def create(cls, B, heads_kv, capacity, d, r=0, *, mass=False, device="cuda"):
@@ -297,34 +262,11 @@ def cache_append(cache, k, v, w=None, *, start, counts=None, stream=None):
     """
     if not isinstance(cache, Cache8):
         raise TypeError("cache must be a Cache8")
-    return _launch(cache.device, stream, _append, cache, k, v, w, start, counts)
-
-
-def _append(cache, k, v, w, start, counts, st):
-    dev, B, Hk, d, r = cache.device, cache.B, cache.Hk, cache.d, cache.r
-    if not isinstance(k, torch.Tensor) or k.dim() != 4:
-        raise ValueError("k must be [B, Hk, n, d]")
-    n = k.shape[2]
-    _require("k", k, torch.bfloat16, (B, Hk, n, d), dev, False)
-    _require("v", v, torch.bfloat16, (B, Hk, n, d), dev, False)
-    if r:
-        _require("w", w, torch.bfloat16, (B, Hk, n, r), dev, False)
-    elif w is not None:
-        raise ValueError("w given, but the cache holds no factors (r = 0)")
-    _require("start", start, torch.int32, (B,), dev)
-    if counts is not None:
-        _require("counts", counts, torch.int32, (B,), dev)
-    sk, sv, sw = k.stride(), v.stride(), w.stride() if r else (0, 0, 0, 1)
-    if sk[3] * sv[3] * sw[3] != 1 or (sk[0] | sk[1] | sk[2] | sv[0] | sv[1] | sv[2] | sw[0] | sw[1]
-                                      | sw[2]) % 8:
-        if n:
-            raise ValueError("k, v and w must have contiguous channels and strides of multiples of 8")
-    strides = _Strides9(sk[0], sk[1], sk[2], sv[0], sv[1], sv[2], sw[0], sw[1], sw[2])
-    rc = load_library().rfb_cache_append(
-        k.data_ptr(), v.data_ptr(), _p(w), ctypes.addressof(strides), *cache._ptrs, _p(cache.mass),
-        start.data_ptr(), _p(counts), B, Hk, n, cache.cap, d, r, st)
-    if rc:
-        _check(rc, "rfb_cache_append")
+    args = (cache._tensors, cache.mass, k, v, w, start, counts)
+    if stream is None:
+        _bind.append(*args)
+    else:
+        _on_stream(cache.device, stream, _bind.append, *args)
     return cache
 
 
@@ -350,58 +292,10 @@ def attn_fwd_cache(q, u, cache, lengths, scale=None, *, causal=True, mass=None, 
     """
     if not isinstance(cache, Cache8):
         raise TypeError("cache must be a Cache8")
-    return _launch(cache.device, stream, _attn, q, u, cache, lengths, scale, causal, mass, mass_out,
-                   decay, out, lse, workspace)
-
-
-def _attn(q, u, cache, lengths, scale, causal, mass, mass_out, decay, out, lse, workspace, st):
-    dev, B, Hk, cap, d, r = cache.device, cache.B, cache.Hk, cache.cap, cache.d, cache.r
-    if not isinstance(q, torch.Tensor) or q.dim() != 4:
-        raise ValueError("q must be [B, H, Nq, d]")
-    _, H, Nq, _ = q.shape
-    _require("q", q, torch.bfloat16, (B, H, Nq, d), dev)
-    if r:
-        _require("u", u, torch.bfloat16, (B, H, Nq, r), dev)
-    elif u is not None:
-        raise ValueError("u given, but the cache holds no factors (r = 0)")
-    if H and (Hk == 0 or H % Hk):
-        raise ValueError(f"{H} query heads are not a multiple of the cache's {Hk}")
-    _require("lengths", lengths, torch.int32, (B,), dev)
-    if mass is not None:
-        if mass_out is None:
-            raise ValueError("mass needs mass_out (which may be the same tensor)")
-        _require("mass", mass, torch.float32, (B, Hk, cap), dev)
-    if mass_out is not None:
-        _require("mass_out", mass_out, torch.float32, (B, Hk, cap), dev)
-    if out is None:
-        out = torch.empty_like(q)
-    else:
-        _require("out", out, torch.bfloat16, (B, H, Nq, d), dev)
-    if lse is None:
-        lse = cache.k_scale.new_empty((B, H, Nq))
-    else:
-        _require("lse", lse, torch.float32, (B, H, Nq), dev)
-    if workspace is None:
-        key = (H, Nq, mass_out is not None)
-        need = cache._workspace_bytes.get(key)
-        if need is None:
-            need = cache._workspace_bytes[key] = attn_cache_workspace_size(cache, *key)
-        workspace = cache.k_scale.new_empty((need + 19) // 4)
-    elif (not isinstance(workspace, torch.Tensor) or workspace.device != dev
-          or not workspace.is_contiguous()):
-        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    rc = load_library().rfb_attn_fwd_cache(
-        q.data_ptr(), _p(u), *cache._ptrs, lengths.data_ptr(), _p(mass), _p(mass_out), decay,
-        out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), B, H, Hk, Nq, cap, d, r,
-        d ** -0.5 if scale is None else scale, 1 if causal else 0, st)
-    if rc == RFB_ERR_WORKSPACE:
-        raise RuntimeError(
-            f"rfb_attn_fwd_cache: workspace of "
-            f"{attn_cache_workspace_size(cache, H, Nq, mass_out is not None)} bytes needed")
-    if rc:
-        _check(rc, "rfb_attn_fwd_cache")
-    return out, lse
+    args = (cache._tensors, q, u, lengths, scale, causal, mass, mass_out, decay, out, lse, workspace)
+    if stream is None:
+        return _bind.attn(*args)
+    return _on_stream(cache.device, stream, _bind.attn, *args)
 
 
 def cache_evict(cache, lengths, keep, recent=0, *, out=None, stream=None):
@@ -419,27 +313,17 @@ def cache_evict(cache, lengths, keep, recent=0, *, out=None, stream=None):
     to = cache if out is None else out
     if not isinstance(to, Cache8):
         raise TypeError("out must be a Cache8")
-    dev, B, Hk = cache.device, cache.B, cache.Hk
+    dev = cache.device
     if cache.mass is None or to.mass is None:
         raise ValueError("eviction needs caches with mass")
-    if (to.device, to.B, to.Hk, to.d, to.r) != (dev, B, Hk, cache.d, cache.r):
+    if (to.device, to.B, to.Hk, to.d, to.r) != (dev, cache.B, cache.Hk, cache.d, cache.r):
         raise ValueError("out must have the cache's device, sequences, heads and channels")
     keep, recent = int(keep), int(recent)
     if not 1 <= keep <= to.cap:
         raise ValueError(f"keep must be in [1, {to.cap}], the receiving capacity")
     if recent < 0:
         raise ValueError("recent must be >= 0")
-    _require("lengths", lengths, torch.int32, (B,), dev)
-    return _launch(dev, stream, _evict, cache, to, lengths, keep, min(recent, keep))
-
-
-def _evict(cache, to, lengths, keep, recent, st):
-    new_lengths = torch.empty_like(lengths)
-    kept = lengths.new_empty((cache.B, cache.Hk, keep))
-    rc = load_library().rfb_cache_evict(
-        *cache._ptrs, cache.mass.data_ptr(), *to._ptrs, to.mass.data_ptr(), lengths.data_ptr(),
-        new_lengths.data_ptr(), kept.data_ptr(), cache.B, cache.Hk, cache.cap, to.cap, cache.d,
-        cache.r, keep, recent, st)
-    if rc:
-        _check(rc, "rfb_cache_evict")
-    return new_lengths, kept
+    args = (cache._tensors, cache.mass, to._tensors, to.mass, lengths, keep, min(recent, keep))
+    if stream is None:
+        return _bind.evict(*args)
+    return _on_stream(dev, stream, _bind.evict, *args)

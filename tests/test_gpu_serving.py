@@ -750,3 +750,52 @@ def test_refusals(rfb_lib, cuda_dev):
     with pytest.raises(RuntimeError, match="status 1"):
         rfb.cache_evict(cache, L, 4, out=mixed)     # in place for some tensors only
     torch.cuda.synchronize()
+
+
+def test_copied_cache_is_its_own(rfb_lib, cuda_dev):
+    """A deep copy or a pickled cache works on its own tensors, a copy on the same."""
+    import copy
+    import io
+    cache, _ = filled(rfb_lib, cuda_dev, 1, 2, 64, 64, 8, seed=151, mass=True)
+    x = step_inputs(cuda_dev, 1, 2, 2, 64, 8, 152)
+    buf = io.BytesIO()
+    torch.save(cache, buf)
+    buf.seek(0)
+    for other in (copy.deepcopy(cache), torch.load(buf, weights_only=False)):
+        before = cache.k.view(torch.uint8).clone()
+        rfb_lib.cache_append(other, x["k"], x["v"], x["w"], start=ints([5], cuda_dev))
+        assert torch.equal(cache.k.view(torch.uint8), before)
+        assert not torch.equal(other.k.view(torch.uint8), before)
+    same = copy.copy(cache)
+    assert same.k is cache.k and same.mass is cache.mass
+    rfb_lib.cache_append(same, x["k"], x["v"], x["w"], start=ints([5], cuda_dev))
+    assert not torch.equal(cache.k.view(torch.uint8), before)
+
+
+def test_replaced_mass_and_other_stream_are_checked(rfb_lib, cuda_dev):
+    cache, _ = filled(rfb_lib, cuda_dev, 2, 2, 64, 64, 0, seed=161, mass=True)
+    x = step_inputs(cuda_dev, 2, 2, 2, 64, 8, 162)
+    L = ints([3, 4], cuda_dev)
+
+    class Elsewhere:
+        device = torch.device("cuda", 77)
+    for call in (lambda: rfb_lib.cache_append(cache, x["k"], x["v"], start=L, stream=Elsewhere()),
+                 lambda: rfb_lib.attn_fwd_cache(x["q"], None, cache, L, stream=Elsewhere()),
+                 lambda: rfb_lib.cache_evict(cache, L, 4, stream=Elsewhere())):
+        with pytest.raises(ValueError, match="stream belongs to"):
+            call()
+    good = cache.mass
+    for bad, err in ((good[:, :1].contiguous(), ValueError), (good.double(), TypeError),
+                     (good.cpu(), ValueError), (good.transpose(1, 2), ValueError), (7, TypeError)):
+        cache.mass = bad
+        with pytest.raises(err, match="mass"):
+            rfb_lib.cache_append(cache, x["k"], x["v"], start=L)
+        with pytest.raises(err, match="mass"):
+            rfb_lib.cache_evict(cache, L, 4)
+    cache.mass = good
+    rfb_lib.cache_append(cache, x["k"], x["v"], start=L)
+    with pytest.raises(TypeError):
+        rfb_lib.attn_fwd_cache(x["q"], None, cache, L, "a quarter")
+    with pytest.raises(TypeError, match="Tensor"):
+        rfb_lib.attn_fwd_cache(x["q"], None, cache, L, out=1)
+    torch.cuda.synchronize()

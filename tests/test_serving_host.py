@@ -90,6 +90,33 @@ def test_python_refuses_host_tensors():
             call()
 
 
+def test_extension_loads_and_refuses(rfb_lib):
+    """The marshalling extension of this build: its symbols resolve, and it refuses before any launch."""
+    from rank_biased_window_b200 import serving
+    bind = serving._load_bind()
+    q = torch.zeros(1, 2, 4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        bind.rotary(q, None, q, q, 0, 1.0, 0, None, None)
+    with pytest.raises(TypeError, match="expected 9 arguments"):
+        bind.rotary(q)
+    # numbers, shapes and types in the messages
+    c = torch.zeros(2, 2, 64, 64, dtype=torch.uint8).view(ref.E4M3)
+    s, n = torch.ones(2, 2, 2), torch.zeros(2, dtype=torch.int32)
+    held = bind.cache(c, c, None, s, s, None)
+    q3 = torch.zeros(2, 3, 1, 64, dtype=torch.bfloat16)
+    for err, match, args in (
+            (ValueError, "3 query heads .* cache's 2", (q3, None, n)),
+            (ValueError, r"lengths has shape \(1,\), expected \(2,\)", (q3[:, :2].contiguous(), None, n[:1])),
+            (ValueError, r"q has shape \(1, 2, 4, 64\), expected \(2, 2, 4, 64\)", (q, None, n)),
+            (TypeError, "q must be torch.bfloat16, got Float", (q3.float(), None, n)),
+            (ValueError, "no factors", (q3, q3, n))):
+        with pytest.raises(err, match=match):
+            bind.attn(held, *args, None, True, None, None, 1.0, None, None, None)
+    for call in (bind.append, bind.attn, bind.evict):
+        with pytest.raises((TypeError, ValueError)):
+            call(*[None] * {bind.append: 7, bind.attn: 12, bind.evict: 7}[call])
+
+
 def test_rotary_frequencies():
     import rank_biased_window_b200 as rfb
     f, a = rfb.rotary_frequencies(64, 10000.0)
