@@ -942,7 +942,8 @@ __device__ __forceinline__ void store_mass(const CacheAttnArgs& a, long long at,
 
 // mass_out = decay mass + sum over the key head's rows of exp(x - LSE).  Up to 8
 // rows leave their scores in the workspace (8 bytes of traffic a row and token, less
-// than reading K again); with more rows the scores are computed again.
+// than reading K again); with more rows the scores are computed again, beside the join
+// where a segment has few partials, else behind it.
 
 // From the scores: the warps of a CTA that share tokens take every
 // mass_row_warps-th row each.
@@ -984,12 +985,39 @@ __device__ __forceinline__ void add_mass(const CacheAttnArgs& a, unsigned ctas, 
     if (t0 + k < L) store_mass(a, static_cast<long long>(bh) * a.cap + t0 + k, add[k]);
 }
 
-// Computed again, in a kernel of its own: a warp holds a block of 32 tokens of K
-// (and W) as MMA row operands and goes over all rows, 64 at a time from shared memory,
-// as the main kernel does but with the final LSE; the weights of a token add up over
-// the lanes of its row.  Everything but the LSE was there before the main kernel began
-// and is prepared before the wait for the join.
+// Computed again: a warp holds a block of 32 tokens of K (and W) as MMA row operands
+// and goes over all rows, 64 at a time from shared memory, as the main kernel does but
+// with the final LSE; the weights of a token add up over the lanes of its row.
+// Everything but the LSE was there before the main kernel began and is prepared before
+// the wait for it.  Two blocks a warp (half the CTAs, 160 registers for 126) measured
+// the same.
 constexpr int kMassChunk = 4 * kCacheBlock;
+constexpr int kMassRows = 64;
+
+// LSE in log2 units of row r0 + threadIdx.x / 2, by two threads, for the 128 of a CTA;
+// +inf for rows that see nothing and for those from r0 + rows on.
+__device__ __forceinline__ float join_lse_row(const CacheAttnArgs& a, const Parts& parts, int bh,
+                                              int r0, int rows) {
+  const int rr = threadIdx.x / 2, seg_rows = min(a.R, a.tile * a.wr);
+  float z = INFINITY;
+  if (rr < rows && parts.n == 1) {
+    z = __ldcg(a.lse + static_cast<long long>(bh) * a.R + r0 + rr) * kLog2e;
+  } else if (rr < rows) {
+    float m = -INFINITY, l = 0.f;
+#pragma unroll 8
+    for (unsigned k = threadIdx.x & 1; k < parts.n; k += 2) {
+      const float2 ml = __ldcg(a.part_ml + parts.index(k, seg_rows, rr));
+      const float mn = fmaxf(m, ml.x), base = mn == -INFINITY ? 0.f : mn;
+      l = l * fast_exp2(m - base) + ml.y * fast_exp2(ml.x - base);
+      m = mn;
+    }
+    const unsigned both = 3u << (threadIdx.x & 30);
+    const float top = fmaxf(m, __shfl_xor_sync(both, m, 1));
+    l *= fast_exp2(m - (top == -INFINITY ? 0.f : top));
+    z = top + __log2f(l + __shfl_xor_sync(both, l, 1));
+  }
+  return z == -INFINITY ? INFINITY : z;
+}
 
 // Pieces of `e4m3 rows` (two, tile_token(g) and 8 behind) of C channels as the MMA's row operand.
 template <int W>
@@ -1001,13 +1029,15 @@ __device__ __forceinline__ void row_operand(const uint32_t (*r)[W], uint32_t (*f
   }
 }
 
-template <int D, int RP>
-__global__ void __launch_bounds__(128) cache_mass_kernel(const CacheAttnArgs a) {
+// FROM_PARTS: the rows' LSE comes from the partials, so that the join of O is not waited
+// for; else from a.lse.
+template <int D, int RP, bool FROM_PARTS>
+__device__ __forceinline__ void recompute_mass(const CacheAttnArgs& a, unsigned ctas, int bh,
+                                               int chunk) {
   constexpr int KW = D / 16, WW = RP / 16;
   __shared__ uint2 sq[8][KW][32], su[WW > 0 ? 8 : 1][WW > 0 ? WW : 1][32];
-  __shared__ float sf[64], sg[64], lse2[64];
-  __shared__ int slim[64];
-  const int bh = blockIdx.x, chunk = blockIdx.y;
+  __shared__ float4 row_of[64];  // factors of K's and W's scores, -LSE, tokens seen
+  __shared__ int fewest[4];      // of the warp's rows, tokens seen by the one that sees fewest
   const int b = bh / a.Hk, warp = warp_id(), lane = lane_id(), g = lane >> 2, t = lane & 3;
   const int L = min(a.lengths[b], a.cap);
   if (chunk * kMassChunk >= L) {
@@ -1061,12 +1091,18 @@ __global__ void __launch_bounds__(128) cache_mass_kernel(const CacheAttnArgs a) 
       }
   }
   float sum[2][2] = {};
+  static_assert(kMassRows == 64, "a segment's rows, where there are several");
   for (int r0 = 0; r0 < a.R; r0 += 64) {
+    Parts parts;
+    if constexpr (FROM_PARTS)
+      parts = parts_of(a, b, (bh - b * a.Hk) * a.row_segs + r0 / kMassRows, ctas);
     const int rows = min(64, a.R - r0);
     if (r0 > 0) __syncthreads();  // the rows before have been read
     uint2 raw[2][KW], raw_u[2][WW > 0 ? WW : 1];
+    int few = L;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+      if (8 * (warp + 4 * i) >= rows) break;
       const long long row = r0 + 8 * (warp + 4 * i) + g, line = static_cast<long long>(bh) * a.R + row;
       fetch_row<D, false>(a.q + line * D, D, row < a.R, t, raw[i]);
       if constexpr (RP > 0) fetch_row<RP, true>(a.u + line * a.r, a.r, row < a.R, t, raw_u[i]);
@@ -1074,6 +1110,7 @@ __global__ void __launch_bounds__(128) cache_mass_kernel(const CacheAttnArgs a) 
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int q = warp + 4 * i, row = r0 + 8 * q + g;
+      if (8 * q >= rows) break;
       uint32_t frag[KW][2], uf[WW > 0 ? WW : 1][2];
       const float f = row_fragments<D>(raw[i], frag) * a.scale_log2;
 #pragma unroll
@@ -1084,20 +1121,23 @@ __global__ void __launch_bounds__(128) cache_mass_kernel(const CacheAttnArgs a) 
 #pragma unroll
         for (int k = 0; k < WW; ++k) su[q][k][lane] = make_uint2(uf[k][0], uf[k][1]);
       }
-      if (t == 0) {
-        const bool live = row < a.R;
-        sf[8 * q + g] = f;
-        sg[8 * q + g] = e;
-        // a row that is none sees nothing
-        slim[8 * q + g] = !live ? 0 : a.causal ? max(min(L, L - a.Nq + 1 + row % a.Nq), 0) : L;
-      }
+      // a row that is none weighs nothing (its LSE is +inf)
+      const int lim = a.causal && row < a.R ? max(min(L, L - a.Nq + 1 + row % a.Nq), 0) : L;
+      few = min(few, lim);
+      if (t == 0) row_of[8 * q + g] = make_float4(f, e, 0.f, __int_as_float(lim));
     }
+    few = __reduce_min_sync(0xffffffffu, few);
+    if (lane == 0) fewest[warp] = few;
     if (r0 == 0) grid_dep_wait();  // the rows' LSE
-    if (threadIdx.x < 64) {
+    __syncthreads();
+    if constexpr (FROM_PARTS) {
+      const float z = join_lse_row(a, parts, bh, r0, rows);
+      if ((threadIdx.x & 1) == 0) row_of[threadIdx.x / 2].z = -z;
+    } else if (threadIdx.x < 64) {
       const float z = threadIdx.x < rows
                           ? __ldcg(a.lse + static_cast<long long>(bh) * a.R + r0 + threadIdx.x) * kLog2e
                           : INFINITY;
-      lse2[threadIdx.x] = z == -INFINITY ? INFINITY : z;
+      row_of[threadIdx.x].z = z == -INFINITY ? -INFINITY : -z;
     }
     __syncthreads();
     if (!busy) continue;
@@ -1108,12 +1148,11 @@ __global__ void __launch_bounds__(128) cache_mass_kernel(const CacheAttnArgs a) 
       row_operand<KW>(kr[j], af[j]);
       if constexpr (RP > 0) row_operand<WW>(wr[j], wf[j]);
     }
+    const bool edge = tok0 + kCacheBlock > min(min(fewest[0], fewest[1]), min(fewest[2], fewest[3]));
 #pragma unroll 2
     for (int q = 0; q < tiles; ++q) {
-      const int row = 8 * q + 2 * t;
-      const float f[2] = {sf[row] * ks, sf[row + 1] * ks};
-      const float z[2] = {lse2[row], lse2[row + 1]};
-      const int lim[2] = {slim[row], slim[row + 1]};
+      const float4 of[2] = {row_of[8 * q + 2 * t], row_of[8 * q + 2 * t + 1]};
+      const float f[2] = {of[0].x * ks, of[1].x * ks}, z[2] = {of[0].z, of[1].z};
       float x[2][4] = {};
 #pragma unroll
       for (int k = 0; k < KW; ++k) {
@@ -1129,24 +1168,30 @@ __global__ void __launch_bounds__(128) cache_mass_kernel(const CacheAttnArgs a) 
           mma_f16(cw[0], wf[0][k], v.x, v.y);
           mma_f16(cw[1], wf[1][k], v.x, v.y);
         }
-        const float e[2] = {sg[row] * ws, sg[row + 1] * ws};
+        const float e[2] = {of[0].y * ws, of[1].y * ws};
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) x[j][k] = fmaf(cw[j][k], e[k & 1], x[j][k] * f[k & 1]);
+          for (int k = 0; k < 4; ++k)
+            x[j][k] = fmaf(cw[j][k], e[k & 1], fmaf(x[j][k], f[k & 1], z[k & 1]));
       } else {
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) x[j][k] *= f[k & 1];
+          for (int k = 0; k < 4; ++k) x[j][k] = fmaf(x[j][k], f[k & 1], z[k & 1]);
+      }
+      if (edge) {
+        const int lim[2] = {__float_as_int(of[0].w), __float_as_int(of[1].w)};
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (tok0 + 16 * j + 8 * (k >> 1) + tile_token(g) >= lim[k & 1]) x[j][k] = -INFINITY;
       }
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const bool sees = tok0 + 16 * j + 8 * (k >> 1) + tile_token(g) < lim[k & 1];
-          sum[j][k >> 1] += sees ? fast_exp2(x[j][k] - z[k & 1]) : 0.f;
-        }
+        for (int k = 0; k < 4; ++k) sum[j][k >> 1] += fast_exp2(x[j][k]);
     }
   }
 #pragma unroll
@@ -1161,11 +1206,18 @@ __global__ void __launch_bounds__(128) cache_mass_kernel(const CacheAttnArgs a) 
     }
 }
 
-// Rows of a CTA of the join: with up to 8 rows a segment one, whose partials go to
-// D / 4 threads each, as many at once as fit; with more, as many rows as fit, each
-// going over its partials in turn.
-__host__ __device__ __forceinline__ int join_rows(int seg_rows, int d) {
-  return seg_rows <= 8 ? 1 : 128 / (d / 4);
+// The weights alone, behind the join.
+template <int D, int RP>
+__global__ void __launch_bounds__(128) cache_mass_kernel(const CacheAttnArgs a) {
+  recompute_mass<D, RP, false>(a, 0, blockIdx.x, blockIdx.y);
+}
+
+// Rows of a CTA of the join: with up to 8 rows or many partials a segment one, whose
+// partials go to D / 4 threads each, as many at once as fit; else as many rows as fit,
+// each going over its partials in turn.
+constexpr int kJoinFew = 16;
+__host__ __device__ __forceinline__ int join_rows(int seg_rows, int d, unsigned partials) {
+  return seg_rows <= 8 || partials > kJoinFew ? 1 : 128 / (d / 4);
 }
 
 template <int D>
@@ -1194,11 +1246,12 @@ __device__ __forceinline__ void join_many(const CacheAttnArgs& a, const Parts& p
   }
   float m = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (unsigned k0 = 0; k0 < parts.n; k0 += 4) {
-    float2 ml[4];
-    float4 v[4];
+  constexpr unsigned AT = 8;  // partials on their way at once
+  for (unsigned k0 = 0; k0 < parts.n; k0 += AT) {
+    float2 ml[AT];
+    float4 v[AT];
 #pragma unroll
-    for (unsigned k = 0; k < 4; ++k) {
+    for (unsigned k = 0; k < AT; ++k) {
       ml[k] = make_float2(-INFINITY, 0.f);
       v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (k0 + k < parts.n) {
@@ -1207,13 +1260,15 @@ __device__ __forceinline__ void join_many(const CacheAttnArgs& a, const Parts& p
         v[k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + p * D + c));
       }
     }
-    const float mn = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), m);
+    float mn = m;
+#pragma unroll
+    for (unsigned k = 0; k < AT; ++k) mn = fmaxf(mn, ml[k].x);
     const float base = mn == -INFINITY ? 0.f : mn, back = fast_exp2(m - base);
     m = mn;
     l *= back;
     acc.x *= back, acc.y *= back, acc.z *= back, acc.w *= back;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (unsigned k = 0; k < AT; ++k) {
       const float f = fast_exp2(ml[k].x - base);
       l = fmaf(ml[k].y, f, l);
       acc.x = fmaf(v[k].x, f, acc.x), acc.y = fmaf(v[k].y, f, acc.y);
@@ -1301,14 +1356,16 @@ __device__ __forceinline__ void join_one(const CacheAttnArgs& a, const Parts& pa
   store_row<D>(a, out, c, m, l, acc);
 }
 
-// Joins the rows and, with scores, adds the weights up: blockIdx.y is a set of rows of
+// Joins the rows and, with mass, adds the weights up: blockIdx.y is a set of `per` rows of
 // the segment blockIdx.x, a (b, h, row segment), or, from `row_sets` on, a chunk of
 // tokens of the key head (taken by its first row segment).  Where the partials lie
 // follows from the lengths alone, which no kernel writes between the main kernel's start
 // and this one, so that is found before the wait for the main kernel.
-template <int D>
+// RP >= 0: the weights are recomputed from K and W, else they come from the scores.
+template <int D, int RP>
 __global__ void __launch_bounds__(128) cache_attn_combine_kernel(const CacheAttnArgs a,
-                                                                 unsigned ctas, int row_sets) {
+                                                                 unsigned ctas, int per,
+                                                                 int row_sets) {
   const int set = blockIdx.y, mult = a.Hk * a.row_segs;
   const int b = blockIdx.x / mult, seg = blockIdx.x - b * mult;
   const int h = seg / a.row_segs, rs = seg - h * a.row_segs, bh = b * a.Hk + h;
@@ -1316,15 +1373,21 @@ __global__ void __launch_bounds__(128) cache_attn_combine_kernel(const CacheAttn
     const Parts parts = parts_of(a, b, seg, ctas);
     grid_dep_wait();
     if (parts.n == 1) return;  // one CTA had it whole
-    const int per = join_rows(min(a.R, a.tile * a.wr), D);
-    if (per == 1)
+    if (RP < 0 && per == 1)
       join_one<D>(a, parts, bh, rs, set);
     else
       join_many<D>(a, parts, bh, rs, set * per);
     return;
   }
-  grid_dep_wait();
-  if (rs == 0) add_mass(a, ctas, bh, set - row_sets);
+  if constexpr (RP >= 0) {
+    if (rs == 0)
+      recompute_mass<D, RP, true>(a, ctas, bh, set - row_sets);
+    else
+      grid_dep_wait();
+  } else {
+    grid_dep_wait();
+    if (rs == 0) add_mass(a, ctas, bh, set - row_sets);
+  }
 }
 
 }  // namespace rfb

@@ -128,14 +128,21 @@ int launch_cache_attn(const CacheAttnArgs& a, const CaPlan& p, cudaStream_t st) 
                  : a.scores   ? launch_cache_attn_main<D, RP, 1, true>(a, p, st)
                               : launch_cache_attn_main<D, RP, 1, false>(a, p, st);
   if (rc != RFB_OK) return rc;
-  const int per = join_rows(p.seg_rows, D), row_sets = (p.seg_rows + per - 1) / per;
+  const unsigned segs = static_cast<unsigned>(a.B * a.Hk * a.row_segs);
+  const unsigned ctas = static_cast<unsigned>(p.ctas), partials = (ctas + segs - 1) / segs;
+  const int per = join_rows(p.seg_rows, D, partials), row_sets = (p.seg_rows + per - 1) / per;
+  const bool again = a.mass_out && !a.scores && a.cap > 0;  // recompute the weights
+  const int again_chunks = (a.cap + kMassChunk - 1) / kMassChunk;
+  if (again && per > 1) {
+    launch_pdl(cache_attn_combine_kernel<D, RP>, dim3(segs, row_sets + again_chunks), dim3(128), 0,
+               st, a, ctas, per, row_sets);
+    return launch_status();
+  }
   const int chunks = a.scores ? (a.cap + mass_tokens(a.R) - 1) / mass_tokens(a.R) : 0;
-  launch_pdl(cache_attn_combine_kernel<D>,
-             dim3(static_cast<unsigned>(a.B * a.Hk * a.row_segs), row_sets + chunks), dim3(128), 0,
-             st, a, static_cast<unsigned>(p.ctas), row_sets);
-  if (a.mass_out && !a.scores && a.cap > 0)
-    launch_pdl(cache_mass_kernel<D, RP>,
-               dim3(static_cast<unsigned>(a.B * a.Hk), (a.cap + kMassChunk - 1) / kMassChunk),
+  launch_pdl(cache_attn_combine_kernel<D, -1>, dim3(segs, row_sets + chunks), dim3(128), 0, st, a,
+             ctas, per, row_sets);
+  if (again)
+    launch_pdl(cache_mass_kernel<D, RP>, dim3(static_cast<unsigned>(a.B * a.Hk), again_chunks),
                dim3(128), 0, st, a);
   return launch_status();
 }

@@ -302,6 +302,22 @@ def test_attention_splits(rfb_lib, cuda_dev, B, Hk, G, cap, top):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])  # the order of joins is fixed
 
 
+@pytest.mark.parametrize("d,r", [(32, 0), (32, 16), (32, 32), (32, 64), (64, 0), (64, 16), (64, 32),
+                                 (64, 64), (128, 0), (128, 16), (128, 32), (128, 64)])
+@pytest.mark.parametrize("B,Hk,H,Nq,cap,lengths", [
+    (3, 2, 4, 9, 512, [512, 77, 5]),          # few partials a segment, one of a single CTA
+    (2, 1, 4, 40, 1024, [1000, 640]),         # the same, three row segments
+    (1, 1, 2, 9, 2048, [2011]),               # many partials a segment
+    (1, 1, 3, 50, 4096, [4095])])             # the same, three row segments
+def test_attention_joins_of_many_rows(rfb_lib, cuda_dev, d, r, B, Hk, H, Nq, cap, lengths):
+    """More than 8 rows a key head with weights kept, which need the joined LSE of every row."""
+    cache, refs = filled(rfb_lib, cuda_dev, B, Hk, cap, d, r, seed=cap + r)
+    mass = torch.rand(B, Hk, cap, generator=gen(3)).to(cuda_dev)
+    a = run_attn(rfb_lib, cuda_dev, cache, refs, lengths, H, Nq, mass=mass, decay=0.5, seed=r)
+    b = run_attn(rfb_lib, cuda_dev, cache, refs, lengths, H, Nq, mass=mass, decay=0.5, seed=r)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 @pytest.mark.parametrize("d", [32, 64, 128])
 def test_attention_scales_far_apart(rfb_lib, cuda_dev, d):
     """Blocks whose scales differ by many powers of two, one of zeros."""
