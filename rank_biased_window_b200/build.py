@@ -67,7 +67,7 @@ def build_bind(force: bool = False) -> str:
            "-isystem", os.path.join(where, "include", "torch", "csrc", "api", "include"),
            "-isystem", os.path.join(cuda, "include"), "-L", os.path.join(where, "lib"),
            "-o", tmp, BIND_SOURCE,
-           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
