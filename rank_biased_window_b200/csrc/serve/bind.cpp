@@ -79,6 +79,25 @@ void require(const char* name, const at::Tensor& t, at::ScalarType dtype, at::In
   refuse(PyExc_ValueError, name, " must be contiguous");
 }
 
+// Whether the memory of two tensors meets: the stretches from their first to their last element.
+bool meet(const at::Tensor& x, const at::Tensor& y) {
+  if (x.numel() == 0 || y.numel() == 0) return false;
+  const auto end = [](const at::Tensor& t) {
+    int64_t last = 0;
+    for (int64_t i = 0; i < t.dim(); ++i) last += (t.size(i) - 1) * t.stride(i);
+    return static_cast<const char*>(t.const_data_ptr()) + (last + 1) * t.element_size();
+  };
+  return static_cast<const char*>(x.const_data_ptr()) < end(y) &&
+         static_cast<const char*>(y.const_data_ptr()) < end(x);
+}
+void apart(const char* name, const at::Tensor& x, const char* other, const at::Tensor& y) {
+  if (meet(x, y)) refuse(PyExc_ValueError, name, " must not share memory with ", other);
+}
+// In place or apart.
+void same_or_apart(const char* name, const at::Tensor& x, const char* other, const at::Tensor& y) {
+  if (x.const_data_ptr() != y.const_data_ptr()) apart(name, x, other, y);
+}
+
 void check(int rc, const char* what) {
   if (rc == RFB_OK) return;
   std::string s = std::string(what) + " failed: " + api.strerror(rc) + " (status " + std::to_string(rc);
@@ -187,6 +206,8 @@ PyObject* rotary(PyObject* const* a) {
   } else {
     qo = tensor(a[7], "q_out");
     require("q_out", qo, dt, q.sizes(), dev);
+    apart("q_out", qo, "q", q);
+    if (has_k) apart("q_out", qo, "k", k);
   }
   if (has_k) {
     if (a[8] == Py_None) {
@@ -194,6 +215,9 @@ PyObject* rotary(PyObject* const* a) {
     } else {
       ko = tensor(a[8], "k_out");
       require("k_out", ko, dt, k.sizes(), dev);
+      apart("k_out", ko, "q", q);
+      apart("k_out", ko, "k", k);
+      apart("k_out", ko, "q_out", qo);
     }
   }
   check(call(api.rotary, q.const_data_ptr(), has_k ? k.const_data_ptr() : nullptr, qo.data_ptr(),
@@ -236,11 +260,12 @@ PyObject* cache(PyObject* const* a) {
   });
 }
 
-float* mass_of(PyObject* o, const Cache& c) {
+const at::Tensor& mass_of(PyObject* o, const Cache& c) {
   const at::Tensor& t = tensor(o, "mass");
   require("mass", t, at::kFloat, {c.B, c.Hk, c.cap}, c.device());
-  return static_cast<float*>(t.data_ptr());
+  return t;
 }
+float* floats(const at::Tensor& t) { return static_cast<float*>(t.data_ptr()); }
 
 // append(cache, mass, k, v, w, start, counts)
 PyObject* append(PyObject* const* a) {
@@ -271,7 +296,7 @@ PyObject* append(PyObject* const* a) {
     require("counts", t, at::kInt, {c.B}, dev);
     counts = static_cast<const int*>(t.const_data_ptr());
   }
-  float* mass = a[1] == Py_None ? nullptr : mass_of(a[1], c);
+  float* mass = a[1] == Py_None ? nullptr : floats(mass_of(a[1], c));
   Launch on(dev);
   check(call(api.append, x[0].const_data_ptr(), x[1].const_data_ptr(),
              c.r ? x[2].const_data_ptr() : nullptr, strides, c.ptr(0), c.ptr(1), c.ptr(2), c.scale(0),
@@ -307,12 +332,13 @@ PyObject* attn(PyObject* const* a) {
   if (a[6] != Py_None) {
     if (a[7] == Py_None)
       refuse(PyExc_ValueError, "mass needs mass_out (which may be the same tensor)");
-    mass = mass_of(a[6], c);
+    mass = floats(mass_of(a[6], c));
   }
   if (a[7] != Py_None) {
     const at::Tensor& t = tensor(a[7], "mass_out");
     require("mass_out", t, at::kFloat, {c.B, c.Hk, c.cap}, dev);
-    mass_out = static_cast<float*>(t.data_ptr());
+    mass_out = floats(t);
+    if (mass) same_or_apart("mass_out", t, "mass", mass_of(a[6], c));
   }
   const double scale = a[4] == Py_None ? 1.0 / std::sqrt(static_cast<double>(c.d)) : number(a[4]);
   const float decay = static_cast<float>(number(a[8]));
@@ -327,6 +353,8 @@ PyObject* attn(PyObject* const* a) {
   } else {
     out = tensor(a[9], "out");
     require("out", out, at::kBFloat16, q.sizes(), dev);
+    apart("out", out, "q", q);
+    if (u) apart("out", out, "u", THPVariable_Unpack(a[2]));
   }
   if (a[10] == Py_None) {
     lse = make({c.B, H, Nq}, at::kFloat, dev);
@@ -357,8 +385,12 @@ PyObject* attn(PyObject* const* a) {
 PyObject* evict(PyObject* const* a) {
   const Cache &c = cache_of(a[0]), &to = cache_of(a[2]);
   const at::Device dev = c.device();
-  const float* mass = mass_of(a[1], c);
-  float* to_mass = mass_of(a[3], to);
+  const at::Tensor &mass = mass_of(a[1], c), &to_mass = mass_of(a[3], to);
+  if (&c != &to) {
+    for (int i = 0; i < 6; ++i)
+      if (c.t[i].defined()) same_or_apart("out", to.t[i], "the cache", c.t[i]);
+    same_or_apart("out", to_mass, "the cache", mass);
+  }
   const at::Tensor& lengths = tensor(a[4], "lengths");
   require("lengths", lengths, at::kInt, {c.B}, dev);
   const int keep = small(integer(a[5]), "keep"), recent = small(integer(a[6]), "recent");
@@ -366,8 +398,8 @@ PyObject* evict(PyObject* const* a) {
   at::Tensor n = make({c.B}, at::kInt, dev);
   at::Tensor kept = make({c.B, c.Hk, keep}, at::kInt, dev);
   check(call(api.evict, c.ptr(0), c.ptr(1), c.ptr(2), c.scale(0), c.scale(1), c.scale(2),
-             mass, to.ptr(0), to.ptr(1), to.ptr(2),
-             to.scale(0), to.scale(1), to.scale(2), to_mass, static_cast<const int*>(lengths.const_data_ptr()), static_cast<int*>(n.data_ptr()),
+             floats(mass), to.ptr(0), to.ptr(1), to.ptr(2),
+             to.scale(0), to.scale(1), to.scale(2), floats(to_mass), static_cast<const int*>(lengths.const_data_ptr()), static_cast<int*>(n.data_ptr()),
              static_cast<int*>(kept.data_ptr()), small(c.B, "B"), small(c.Hk, "Hk"),
              small(c.cap, "capacity"), small(to.cap, "capacity"), static_cast<int>(c.d),
              static_cast<int>(c.r), keep, recent, on.stream),

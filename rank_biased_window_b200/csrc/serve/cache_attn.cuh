@@ -1206,6 +1206,14 @@ __device__ __forceinline__ void recompute_mass(const CacheAttnArgs& a, unsigned 
     }
 }
 
+// No query: what is there decays.
+__global__ void __launch_bounds__(128) cache_decay_kernel(const CacheAttnArgs a) {
+  grid_dep_wait();
+  const int t = blockIdx.y * 128 + threadIdx.x;
+  if (t < min(a.lengths[blockIdx.x / a.Hk], a.cap))
+    store_mass(a, static_cast<long long>(blockIdx.x) * a.cap + t, 0.f);
+}
+
 // The weights alone, behind the join.
 template <int D, int RP>
 __global__ void __launch_bounds__(128) cache_mass_kernel(const CacheAttnArgs a) {

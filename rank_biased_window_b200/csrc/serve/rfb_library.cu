@@ -324,9 +324,21 @@ int rfb_attn_fwd_cache(const void* q, const void* u, const void* k8, const void*
   if (heads < 0 || Nq < 0 || !std::isfinite(scale) || !(scale > 0.f) || !std::isfinite(decay))
     return RFB_ERR_INVALID_ARG;
   if (int rc = check_cache(B, heads_kv, cap, d, r)) return rc;
-  if (B == 0 || heads == 0 || Nq == 0) return RFB_OK;
+  if (B == 0 || ((heads == 0 || Nq == 0) && (!mass_out || heads_kv == 0 || cap == 0))) return RFB_OK;
   if (heads_kv == 0 || heads % heads_kv != 0) return RFB_ERR_INVALID_ARG;
   const long long R = static_cast<long long>(heads / heads_kv) * Nq;
+  if (R == 0) {
+    if (cap > 65535 * 128) return RFB_ERR_UNSUPPORTED;
+    if (!lengths) return RFB_ERR_INVALID_ARG;
+    if (!aligned16(mass) || !aligned16(mass_out) || !aligned_to(lengths, 4)) return RFB_ERR_ALIGNMENT;
+    CacheAttnArgs a = {};
+    a.lengths = lengths;
+    a.mass = mass, a.mass_out = mass_out, a.decay = decay;
+    a.Hk = heads_kv, a.cap = cap;
+    launch_pdl(cache_decay_kernel, dim3(static_cast<unsigned>(B * heads_kv), (cap + 127) / 128),
+               dim3(128), 0, static_cast<cudaStream_t>(stream), a);
+    return launch_status();
+  }
   if (R > (1LL << 24) || static_cast<long long>(B) * heads_kv * ((R + 7) / 8) > 0x7fffffffLL / (cap / kCacheBlock + 8) ||
       (mass_out && cap > 65000 * 128))
     return RFB_ERR_UNSUPPORTED;

@@ -145,7 +145,8 @@ def rotary_fwd(q, k, positions, freqs, *, layout="half", amplitude=1.0, q_out=No
 
     q and k may be views with any batch, head and token strides (for example
     [B, N, H, d] transposed), so that the rotation also brings them into the
-    layout that attention takes.  positions: int32 [N] or [B, N]; freqs: fp64
+    layout that attention takes; q_out and k_out must not share memory with
+    them.  positions: int32 [N] or [B, N]; freqs: fp64
     [rot / 2] from rotary_frequencies (channels from rot on pass through).
     """
     return _rotary(q, k, positions, freqs, layout, amplitude, 0, q_out, k_out, stream)
@@ -288,7 +289,8 @@ def attn_fwd_cache(q, u, cache, lengths, scale=None, *, causal=True, mass=None, 
     query without tokens gets O = 0 and LSE = -inf.  mass_out (fp32 [B, Hk,
     cap]) receives decay * mass + the softmax weights that each token got,
     summed over the queries of its head; it may be mass itself (cache.mass, to
-    gather what cache_evict goes by), and mass None counts as zeros.
+    gather what cache_evict goes by), and mass None counts as zeros.  out must
+    not share memory with q or u.
     """
     if not isinstance(cache, Cache8):
         raise TypeError("cache must be a Cache8")

@@ -768,6 +768,57 @@ def test_refusals(rfb_lib, cuda_dev):
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("H,Nq", [(2, 0), (0, 1)])
+def test_attention_without_queries_decays_the_mass(rfb_lib, cuda_dev, H, Nq):
+    cache, _ = filled(rfb_lib, cuda_dev, 4, 2, 224, 64, 8, seed=191, mass=True)
+    lengths = [0, 1, 200, 500]
+    q = torch.empty(4, H, Nq, 64, dtype=torch.bfloat16, device=cuda_dev)
+    u = torch.empty(4, H, Nq, 8, dtype=torch.bfloat16, device=cuda_dev)
+    mass = torch.rand(4, 2, 224, generator=gen(192)).to(cuda_dev)
+    for before, decay in ((mass, 0.5), (None, 1.0)):
+        got = torch.full_like(mass, 123.0)
+        o, lse = rfb_lib.attn_fwd_cache(q, u, cache, ints(lengths, cuda_dev), mass=before, mass_out=got,
+                                        decay=decay)
+        assert o.shape == q.shape and lse.shape == q.shape[:3]
+        for b, L in enumerate([0, 1, 200, 224]):
+            want = mass[b, :, :L] * 0.5 if before is not None else torch.zeros_like(mass[b, :, :L])
+            assert torch.equal(got[b, :, :L], want) and bool((got[b, :, L:] == 123.0).all())
+
+
+def test_shared_memory_is_refused(rfb_lib, cuda_dev):
+    """Outputs that lie in the inputs' memory; in place is for the mass and for eviction."""
+    x = step_inputs(cuda_dev, 1, 2, 2, 64, 8, 201)
+    pos, L = ints([3], cuda_dev), ints([40], cuda_dev)
+    f, _ = rfb_lib.rotary_frequencies(64, device=cuda_dev)
+    cache, _ = filled(rfb_lib, cuda_dev, 1, 1, 96, 64, 8, seed=202, mass=True)
+    q2 = x["q"][:, :1].contiguous()
+    both = torch.zeros(2 * 96, device=cuda_dev)
+
+    def behind(name, n):  # a cache of 64 tokens within the other's 96
+        return getattr(cache, name)[:, :, n:]
+    part = rfb_lib.Cache8(behind("k", 32), behind("v", 32), behind("w", 32), behind("k_scale", 1),
+                          behind("v_scale", 1), behind("w_scale", 1), behind("mass", 32))
+    for call in (lambda: rfb_lib.rotary_fwd(x["q"], x["k"], pos, f, q_out=x["q"]),
+                 lambda: rfb_lib.rotary_fwd(x["q"], x["k"], pos, f, q_out=x["k"]),
+                 lambda: rfb_lib.rotary_fwd(x["q"], x["k"], pos, f, k_out=x["k"]),
+                 lambda: rfb_lib.attn_fwd_cache(q2, x["u"][:, :1].contiguous(), cache, L, out=q2),
+                 lambda: rfb_lib.attn_fwd_cache(
+                     q2, x["u"][:, :1].contiguous(), cache, L, mass=both[:96].view(1, 1, 96),
+                     mass_out=both[32:128].view(1, 1, 96)),
+                 lambda: rfb_lib.cache_evict(cache, L, 8, out=part)):
+        with pytest.raises(ValueError, match="share memory"):
+            call()
+    same = torch.zeros(1, 1, 96, device=cuda_dev)
+    rfb_lib.attn_fwd_cache(q2, x["u"][:, :1].contiguous(), cache, L, mass=same, mass_out=same)
+    # halves of one buffer are apart
+    pair = torch.empty(2, *x["q"].shape, dtype=torch.bfloat16, device=cuda_dev)
+    pair[0] = x["q"]
+    a, _ = rfb_lib.rotary_fwd(pair[0], None, pos, f, q_out=pair[1])
+    b, _ = rfb_lib.rotary_fwd(x["q"], None, pos, f)
+    assert torch.equal(a, b)
+    torch.cuda.synchronize()
+
+
 def test_copied_cache_is_its_own(rfb_lib, cuda_dev):
     """A deep copy or a pickled cache works on its own tensors, a copy on the same."""
     import copy
