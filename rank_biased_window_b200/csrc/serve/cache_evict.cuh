@@ -13,6 +13,10 @@
 // written once the blocks up to it have been read, and every later block's rows
 // lie behind it.  A block whose tokens all stay is left as it is; others get the
 // scale of their own values.
+//
+// The move is bound by HBM, the selection by latency (a few thousand keys a CTA, four
+// digits, a meeting of the cluster for each): 64 heads of up to 16384 tokens, d = 128, cut
+// to 8192 take 55.5 us, of which the selection 13 (under ncu); 8 heads of 1000 tokens 9 us.
 #pragma once
 #include "../sm100.cuh"
 #include "e4m3.cuh"
