@@ -947,7 +947,8 @@ __device__ __forceinline__ void store_mass(const CacheAttnArgs& a, long long at,
 
 // mass_out = decay mass + sum over the key head's rows of exp(x - LSE).  Up to 8
 // rows leave their scores in the workspace (8 bytes of traffic a row and token, less
-// than reading K again); with more rows the scores are computed again, beside the join
+// than reading K again: a decode step 24.0 us against 37.1, 8 rows a key head 15.1
+// against 17.5); with more rows the scores are computed again, beside the join
 // where a segment has few partials, else behind it.
 
 // From the scores: the warps of a CTA that share tokens take every
@@ -1227,7 +1228,9 @@ __global__ void __launch_bounds__(128) cache_mass_kernel(const CacheAttnArgs a) 
 
 // Rows of a CTA of the join: with up to 8 rows or many partials a segment one, whose
 // partials go to D / 4 threads each, as many at once as fit; else as many rows as fit,
-// each going over its partials in turn.
+// each going over its partials in turn (64 rows of 14 partials, with the weights beside
+// the join: 30.7 us against 34.0 one by one; 16 rows of 56: 38.8 against 30.5, of 222:
+// 86 against 64).
 constexpr int kJoinFew = 16;
 __host__ __device__ __forceinline__ int join_rows(int seg_rows, int d, unsigned partials) {
   return seg_rows <= 8 || partials > kJoinFew ? 1 : 128 / (d / 4);

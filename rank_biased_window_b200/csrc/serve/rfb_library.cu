@@ -37,7 +37,8 @@ int launch_rotary(RotArgs& a, int B, int sms, cudaStream_t st) {
   a.units = a.rot / (2 * pairs) + (a.d - a.rot) / (VEC ? Rot<T>::VEC : 1);
   // One thread per unit and group of heads.  More heads a thread share the
   // sine and cosine; fewer fill the chip: halve the group until there are 512
-  // threads an SM (below that the call is latency, and one head is shortest).
+  // threads an SM (below that the call is latency, and one head is shortest).  One head a
+  // thread: 103 us for 47 at 2 x 16384 tokens; all heads: 6.4 us for 6.0 at one.
   const int heads = a.heads[0] + a.heads[1];
   const double units = static_cast<double>(B) * a.N * a.units;
   int per = heads;
@@ -88,6 +89,7 @@ size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 CaPlan plan_cache_attn(int B, int Hk, int R, int cap, int d, int r, bool mass, int sms) {
   CaPlan p;
+  // Up to 8 rows in a tile of 16 would be half empty: 44.5 us for 34.1 (4 rows, d = 128).
   p.tile = R <= 8 ? 8 : 16;
   const int tiles = (R + p.tile - 1) / p.tile;
   p.wr = tiles >= 3 ? 4 : tiles;
@@ -434,7 +436,8 @@ int rfb_cache_evict(const void* k8, const void* v8, const void* w8, const float*
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int bh = B * heads_kv;
   // A cluster of CTAs a (sequence, head) while that leaves SMs without one and
-  // each CTA a few thousand tokens, or where the keys of one do not fit.
+  // each CTA a few thousand tokens, or where the keys of one do not fit (8 heads of 65536
+  // tokens: 60.6 us by one CTA each, 18.4 by eight; of 1024: 9.8 by one, 12.4 by eight).
   int parts = 1;
   while (parts < 8 && ((2 * parts * bh <= dev.sms && cap > 2048 * parts) ||
                        cap > parts * kSelMaxKeys * kSelThreads))
