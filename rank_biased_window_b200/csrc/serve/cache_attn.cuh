@@ -29,9 +29,11 @@
 // Work split: the blocks of all (sequence, key head, row tile) segments form one
 // line, cut into equal parts, one per CTA, so ragged lengths and few long
 // sequences fill the chip alike; a segment counts kCaSegmentCost blocks more than
-// it has, since beginning one and joining its warps takes that long.  A segment that one CTA holds whole is finished
-// there; others leave (max, sum, O) partials, which cache_attn_combine_kernel
-// joins in order (results do not depend on timing).
+// it has, since beginning one and joining its warps takes that long.  A segment that
+// one CTA holds whole is finished there; others leave (max, sum, O) partials, which
+// cache_attn_combine_kernel joins in order (results do not depend on timing).  Short
+// contexts, and segments enough for several waves, take a CTA a segment instead
+// (`whole`): no partials, no join.
 #pragma once
 #include "../sm100.cuh"
 #include "e4m3.cuh"
@@ -63,6 +65,7 @@ struct CacheAttnArgs {
   int wr;        // warps over row tiles: 1, 2 or 4
   int row_segs;  // segments of tile * wr rows
   int causal;
+  int whole;     // one CTA a segment, no partials
   int stages;
   float scale_log2;
   int* err_word;
@@ -152,6 +155,16 @@ __device__ __forceinline__ Place place_of(const CacheAttnArgs& a, unsigned mult)
   p.seg = in_seq / len;
   p.in = in_seq - p.seg * len;
   p.nb = len - kCaSegmentCost;
+  return p;
+}
+
+// The same with a CTA a segment; an empty one has nb = 0.
+__device__ __forceinline__ Place segment_of(const CacheAttnArgs& a, unsigned mult) {
+  Place p = {};
+  p.b = blockIdx.x / mult;
+  p.seg = blockIdx.x - p.b * mult;
+  p.nb = cache_blocks(a, p.b);
+  p.stop = line_length(p.nb);
   return p;
 }
 
@@ -395,6 +408,17 @@ __device__ __forceinline__ void pv_edge(const uint32_t (*p)[QT][2], uint32_t vro
   }
 }
 
+// The rows of a segment without tokens.
+template <int D>
+__device__ __forceinline__ void empty_rows(const CacheAttnArgs& a, const Place& p, int tile) {
+  const int h = p.seg / a.row_segs, rs = p.seg - h * a.row_segs, first = rs * a.wr * tile;
+  const int rows = min(a.R - first, a.wr * tile);
+  const long long row = (static_cast<long long>(p.b) * a.Hk + h) * a.R + first;
+  uint4* o = reinterpret_cast<uint4*>(a.o + row * D);
+  for (int i = threadIdx.x; i < rows * (D / 8); i += kCaThreads) o[i] = make_uint4(0, 0, 0, 0);
+  for (int i = threadIdx.x; i < rows; i += kCaThreads) a.lse[row + i] = -INFINITY;
+}
+
 // QT: tiles of 8 queries a warp holds.
 template <int D, int RP, int QT, bool MASS>
 __global__ void __launch_bounds__(kCaThreads, 3)
@@ -425,11 +449,14 @@ __global__ void __launch_bounds__(kCaThreads, 3)
   const WaitGuard guard{&head.abort_flag, a.err_word, a.wait_ns, a.fail_site};
   grid_dep_wait();
   const int mult = a.Hk * a.row_segs;
-  const Place place = place_of(a, mult);
+  const Place place = a.whole ? segment_of(a, mult) : place_of(a, mult);
   grid_dep_launch_next();
   unsigned at = place.at;
   const unsigned stop = place.stop;
-  if (at >= stop) return;
+  if (at >= stop) {
+    if (a.whole) empty_rows<D>(a, place, QR);
+    return;
+  }
   int b = place.b, nb = place.nb, seg = place.seg;
   // this CTA's blocks [blk0, blk1) of the segment; none where its part ends within the cost
   const auto first_block = [](unsigned in) {
@@ -460,7 +487,7 @@ __global__ void __launch_bounds__(kCaThreads, 3)
     // the segment after this one
     const unsigned next_at = at + (nb + kCaSegmentCost - in);
     int nseg = seg + 1, nxb = b, nnb = nb;
-    if (nseg == mult) {
+    if (nseg == mult && next_at < stop) {
       nseg = 0;
       do {
         ++nxb;
@@ -887,6 +914,7 @@ struct Parts {
   }
 };
 __device__ __forceinline__ Parts parts_of(const CacheAttnArgs& a, int b, int seg, unsigned ctas) {
+  if (a.whole) return Parts{0, cache_blocks(a, b) > 0 ? 1u : 0u, 0};
   const int mult = a.Hk * a.row_segs;
   unsigned before, total;
   count_line(a, b, before, total);

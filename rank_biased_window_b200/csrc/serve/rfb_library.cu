@@ -81,7 +81,7 @@ int check_cache(int B, int heads_kv, int cap, int d, int r) {
 
 // Row tiles and CTAs of the attention over the cache.
 struct CaPlan {
-  int tile, wr, row_segs, seg_rows, ctas, stages, smem;
+  int tile, wr, row_segs, seg_rows, ctas, stages, smem, whole;
   size_t ml_bytes, o_bytes, score_bytes;
 };
 
@@ -108,8 +108,21 @@ CaPlan plan_cache_attn(int B, int Hk, int R, int cap, int d, int r, bool mass, i
   p.stages = fit(resident) < kCaMaxStages ? fit(resident) : kCaMaxStages;
   p.smem = kCaRing + p.stages * stage * wts;
   p.ctas = static_cast<int>(most < wave ? (most > 0 ? most : 1) : wave);
-  p.ml_bytes = round256(static_cast<size_t>(p.ctas) * 2 * p.seg_rows * sizeof(float2));
-  p.o_bytes = round256(static_cast<size_t>(p.ctas) * 2 * p.seg_rows * d * sizeof(float));
+  // A CTA a segment, which needs no join of partials and lets the hardware even out the
+  // CTAs: for short contexts and for segments that fill several waves.  Measured over
+  // 0.02 to 8 waves of segments (1 to 450 sequences of 8 heads, d = 64): up to four blocks a
+  // group of warps always (16 sequences to 128 tokens 5.7 us for 10.4, one of 500 tokens 7.0 for
+  // 8.2, of 1000 10.4 for 8.5), else up to 16 for each wave of segments (450 sequences to 4096
+  // tokens 194 us for 244, 225 to 1024 39 for 53, but 28 to 2048 20.2 for 15.7).  The same with
+  // the mass, whose second kernel runs in any case (112 sequences to 512 tokens 19.3 us for
+  // 24.5, one of 500 10.4 for 9.9), so that O and LSE do not depend on it.
+  const long long segs = static_cast<long long>(B) * Hk * p.row_segs;
+  const long long group = (cap / kCacheBlock + wts - 1) / wts;
+  p.whole = group <= 4 || group * wave <= 16 * segs;
+  if (p.whole) p.ctas = static_cast<int>(segs);
+  const size_t parts = p.whole ? 0 : static_cast<size_t>(p.ctas) * 2 * p.seg_rows;
+  p.ml_bytes = round256(parts * sizeof(float2) + 1);
+  p.o_bytes = round256(parts * d * sizeof(float));
   p.score_bytes = mass && p.tile == 8 ? static_cast<size_t>(B) * Hk * R * cap * sizeof(float) : 0;
   return p;
 }
@@ -135,14 +148,16 @@ int launch_cache_attn(const CacheAttnArgs& a, const CaPlan& p, cudaStream_t st) 
   const int per = join_rows(p.seg_rows, D, partials), row_sets = (p.seg_rows + per - 1) / per;
   const bool again = a.mass_out && !a.scores && a.cap > 0;  // recompute the weights
   const int again_chunks = (a.cap + kMassChunk - 1) / kMassChunk;
-  if (again && per > 1) {
+  if (again && per > 1 && !a.whole) {
     launch_pdl(cache_attn_combine_kernel<D, RP>, dim3(segs, row_sets + again_chunks), dim3(128), 0,
                st, a, ctas, per, row_sets);
     return launch_status();
   }
   const int chunks = a.scores ? (a.cap + mass_tokens(a.R) - 1) / mass_tokens(a.R) : 0;
-  launch_pdl(cache_attn_combine_kernel<D, -1>, dim3(segs, row_sets + chunks), dim3(128), 0, st, a,
-             ctas, per, row_sets);
+  const int joins = a.whole ? 0 : row_sets;
+  if (joins + chunks > 0)
+    launch_pdl(cache_attn_combine_kernel<D, -1>, dim3(segs, joins + chunks), dim3(128), 0, st, a,
+               ctas, per, joins);
   if (again)
     launch_pdl(cache_mass_kernel<D, RP>, dim3(static_cast<unsigned>(a.B * a.Hk), again_chunks),
                dim3(128), 0, st, a);
@@ -313,6 +328,7 @@ size_t rfb_attn_fwd_cache_workspace_size(int B, int heads, int heads_kv, int Nq,
   if (B == 0 || R == 0 || R > 0x7fffffffLL) return 0;
   DeviceInfo dev;
   if (current_device(&dev)) return 0;
+  // r = 0 needs the most: factors make stages larger, waves smaller, and a CTA a segment likelier
   const CaPlan p = plan_cache_attn(B, heads_kv, static_cast<int>(R), cap, d, 0, with_mass != 0, dev.sms);
   return p.ml_bytes + p.o_bytes + p.score_bytes;
 }
@@ -376,6 +392,7 @@ int rfb_attn_fwd_cache(const void* q, const void* u, const void* k8, const void*
   a.B = B, a.Hk = heads_kv, a.R = static_cast<int>(R), a.Nq = Nq, a.cap = cap, a.r = r;
   a.tile = p.tile, a.wr = p.wr, a.row_segs = p.row_segs;
   a.causal = causal;
+  a.whole = p.whole;
   a.stages = p.stages;
   a.err_word = dev.err_word;
   a.wait_ns = g_wait_limit_ns.load();

@@ -318,6 +318,33 @@ def test_attention_joins_of_many_rows(rfb_lib, cuda_dev, d, r, B, Hk, H, Nq, cap
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("d,r", [(32, 0), (32, 40), (64, 8), (64, 64), (128, 0), (128, 32)])
+@pytest.mark.parametrize("B,Hk,H,Nq,cap,keep_mass", [
+    (5, 2, 6, 1, 512, False),       # short contexts, some empty
+    (5, 1, 4, 5, 256, False),       # 20 rows
+    (4, 1, 2, 70, 128, False),      # several row segments, rows that see nothing
+    (4, 1, 2, 70, 32, True),        # the same, one block
+    (5, 2, 6, 1, 128, True),
+    (130, 4, 4, 1, 160, True),      # more segments than CTAs at once
+    (120, 4, 4, 1, 736, False)])    # the same, several blocks a warp
+def test_attention_of_whole_segments(rfb_lib, cuda_dev, d, r, B, Hk, H, Nq, cap, keep_mass):
+    """Segments that one CTA holds whole, without a join: every length of interest, none among them."""
+    lengths = [(0, 1, cap, cap - 33, 31, cap // 2 + 1, 40)[b % 7] for b in range(B)]
+    lengths = [max(0, min(n, cap)) for n in lengths]
+    cache, refs = filled(rfb_lib, cuda_dev, B, Hk, cap, d, r, seed=cap + r)
+    mass = torch.rand(B, Hk, cap, generator=gen(4)).to(cuda_dev) if keep_mass else None
+    o, lse = run_attn(rfb_lib, cuda_dev, cache, refs, lengths, H, Nq, mass=mass, seed=d)
+    assert bool((o[0] == 0).all()) and bool((lse[0] == float("-inf")).all())
+    size = rfb_lib.attn_cache_workspace_size(cache, H, Nq, keep_mass)
+    ws = torch.empty(size + 64, dtype=torch.uint8, device=cuda_dev)[:size]
+    q = torch.randn(B, H, Nq, d, generator=gen(5)).bfloat16().to(cuda_dev)
+    u = torch.randn(B, H, Nq, r, generator=gen(6)).bfloat16().to(cuda_dev) if r else None
+    L, out = ints(lengths, cuda_dev), torch.full_like(mass, 3.0) if keep_mass else None
+    a = rfb_lib.attn_fwd_cache(q, u, cache, L, mass_out=out, workspace=ws)   # the size is enough
+    b = rfb_lib.attn_fwd_cache(q, u, cache, L, causal=True)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 @pytest.mark.parametrize("d", [32, 64, 128])
 def test_attention_scales_far_apart(rfb_lib, cuda_dev, d):
     """Blocks whose scales differ by many powers of two, one of zeros."""
