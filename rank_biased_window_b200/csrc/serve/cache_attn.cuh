@@ -1022,9 +1022,7 @@ __device__ __forceinline__ void add_mass(const CacheAttnArgs& a, unsigned ctas, 
 // Computed again: a warp holds a block of 32 tokens of K (and W) as MMA row operands
 // and goes over all rows, 64 at a time from shared memory, as the main kernel does but
 // with the final LSE; the weights of a token add up over the lanes of its row.
-// Everything but the LSE was there before the main kernel began and is prepared before
-// the wait for it.  Two blocks a warp (half the CTAs, 160 registers for 126) measured
-// the same.
+// Two blocks a warp (half the CTAs, 160 registers for 126) measured the same.
 constexpr int kMassChunk = 4 * kCacheBlock;
 constexpr int kMassRows = 64;
 
@@ -1074,10 +1072,7 @@ __device__ __forceinline__ void recompute_mass(const CacheAttnArgs& a, unsigned 
   __shared__ int fewest[4];      // of the warp's rows, tokens seen by the one that sees fewest
   const int b = bh / a.Hk, warp = warp_id(), lane = lane_id(), g = lane >> 2, t = lane & 3;
   const int L = min(a.lengths[b], a.cap);
-  if (chunk * kMassChunk >= L) {
-    grid_dep_wait();
-    return;
-  }
+  if (chunk * kMassChunk >= L) return;
   const int blk = chunk * 4 + warp, tok0 = blk * kCacheBlock;
   const bool busy = tok0 < L;
   // the block, on its way while the rows are prepared
@@ -1162,7 +1157,6 @@ __device__ __forceinline__ void recompute_mass(const CacheAttnArgs& a, unsigned 
     }
     few = __reduce_min_sync(0xffffffffu, few);
     if (lane == 0) fewest[warp] = few;
-    if (r0 == 0) grid_dep_wait();  // the rows' LSE
     __syncthreads();
     if constexpr (FROM_PARTS) {
       const float z = join_lse_row(a, parts, bh, r0, rows);
@@ -1251,6 +1245,7 @@ __global__ void __launch_bounds__(128) cache_decay_kernel(const CacheAttnArgs a)
 // The weights alone, behind the join.
 template <int D, int RP>
 __global__ void __launch_bounds__(128) cache_mass_kernel(const CacheAttnArgs a) {
+  grid_dep_wait();
   recompute_mass<D, RP, false>(a, 0, blockIdx.x, blockIdx.y);
 }
 
@@ -1402,9 +1397,9 @@ __device__ __forceinline__ void join_one(const CacheAttnArgs& a, const Parts& pa
 
 // Joins the rows and, with mass, adds the weights up: blockIdx.y is a set of `per` rows of
 // the segment blockIdx.x, a (b, h, row segment), or, from `row_sets` on, a chunk of
-// tokens of the key head (taken by its first row segment).  Where the partials lie
-// follows from the lengths alone, which no kernel writes between the main kernel's start
-// and this one, so that is found before the wait for the main kernel.
+// tokens of the key head (taken by its first row segment).  Nothing is read before the
+// wait for the main kernel, not even what a kernel before that one wrote (lengths, K, W,
+// queries): it is the wait that makes earlier writes visible here.
 // RP >= 0: the weights are recomputed from K and W, else they come from the scores.
 template <int D, int RP>
 __global__ void __launch_bounds__(128) cache_attn_combine_kernel(const CacheAttnArgs a,
@@ -1413,9 +1408,9 @@ __global__ void __launch_bounds__(128) cache_attn_combine_kernel(const CacheAttn
   const int set = blockIdx.y, mult = a.Hk * a.row_segs;
   const int b = blockIdx.x / mult, seg = blockIdx.x - b * mult;
   const int h = seg / a.row_segs, rs = seg - h * a.row_segs, bh = b * a.Hk + h;
+  grid_dep_wait();
   if (set < row_sets) {
     const Parts parts = parts_of(a, b, seg, ctas);
-    grid_dep_wait();
     if (parts.n == 1) return;  // one CTA had it whole
     if (RP < 0 && per == 1)
       join_one<D>(a, parts, bh, rs, set);
@@ -1423,15 +1418,11 @@ __global__ void __launch_bounds__(128) cache_attn_combine_kernel(const CacheAttn
       join_many<D>(a, parts, bh, rs, set * per);
     return;
   }
-  if constexpr (RP >= 0) {
-    if (rs == 0)
-      recompute_mass<D, RP, true>(a, ctas, bh, set - row_sets);
-    else
-      grid_dep_wait();
-  } else {
-    grid_dep_wait();
-    if (rs == 0) add_mass(a, ctas, bh, set - row_sets);
-  }
+  if (rs != 0) return;
+  if constexpr (RP >= 0)
+    recompute_mass<D, RP, true>(a, ctas, bh, set - row_sets);
+  else
+    add_mass(a, ctas, bh, set - row_sets);
 }
 
 }  // namespace rfb
