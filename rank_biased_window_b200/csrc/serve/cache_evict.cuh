@@ -377,8 +377,10 @@ struct MoveWalk {
   struct At {
     int z, bh, block;
   };
-  __device__ __forceinline__ At at(int round) const {
-    const long long item = first + round * step;
+  // Rounds behind the last item, which are looked at a round ahead (but have no source),
+  // are held at the last one, so that every place names a tensor and a head that exist.
+  __host__ __device__ __forceinline__ At at(int round) const {
+    const long long on = first + round * step, item = on < items ? on : items - 1;
     if (IN_PLACE) return At{z0, bh0, static_cast<int>(item)};
     const unsigned head = static_cast<unsigned>(item / per_head);
     const int block = static_cast<int>(item - static_cast<long long>(head) * per_head);

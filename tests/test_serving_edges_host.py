@@ -36,3 +36,43 @@ def test_kernels_wait_before_they_read(name):
         for read in ("__ld", "parts_of", "place_of", "segment_of", "select_begin", "a.lengths", "a.mass",
                      "a.kept", "a.pos[", "a.start[", "_mass<", "fetch", "bulk_load"):
             assert read not in before, (head, read)
+
+
+WALK = r"""
+#include "serve/cache_evict.cuh"
+#include <cstdio>
+int main() {
+  rfb::EvictArgs a = {};
+  int bad = 0;
+  for (int heads : {1, 3, 64})
+    for (int per_head : {1, 5, 33})
+      for (int z0 : {0, 2})
+        for (long long warps : {1, 8, 1184}) {
+          a.heads = heads;
+          const long long items = (long long)heads * per_head * (z0 == 0 ? 2 : 1);
+          for (long long first = 0; first < warps; first += 7) {
+            const int rounds = first < items ? (int)((items - first + warps - 1) / warps) : 0;
+            const rfb::MoveWalk<false> w{a, z0, 0, first, warps, items, rounds, per_head};
+            for (int round = 0; round < rounds + rfb::kMoveStages; ++round) {
+              const auto p = w.at(round);
+              bad += p.z < z0 || p.z > (z0 == 0 ? 1 : 2) || p.bh < 0 || p.bh >= heads ||
+                     p.block < 0 || p.block >= per_head;
+            }
+          }
+        }
+  std::printf("%d\n", bad);
+  return bad != 0;
+}
+"""
+
+
+def test_eviction_walk_names_only_what_exists(tmp_path):
+    """The move's warps look up to two rounds past their last item: tensor, head and
+    block have to exist there too."""
+    import subprocess
+    from rank_biased_window_b200 import build
+    src, exe = tmp_path / "walk.cu", tmp_path / "walk"
+    src.write_text(WALK)
+    subprocess.run([build._nvcc(), *build.ARCH, "-std=c++17", "--expt-relaxed-constexpr", "-I", build.CSRC,
+                    "-o", str(exe), str(src)], check=True, capture_output=True)
+    assert subprocess.run([str(exe)], capture_output=True, text=True).stdout == "0\n"
