@@ -7,6 +7,7 @@ from tests import _serving_ref as ref
 from tests.test_gpu_serving import filled, gen, ints
 
 pytestmark = pytest.mark.gpu
+NAN = float("nan")
 
 
 @pytest.mark.parametrize("d,r,H,Hk,Nq,cap", [
@@ -49,3 +50,90 @@ def test_weights_of_just_appended_tokens(rfb_lib, cuda_dev, d, r, H, Hk, Nq, cap
         ref.assert_within(f"lse {i}", got[i][1], lse, room[1])
         for b, L in enumerate(lengths):
             ref.assert_within(f"mass {i}", outs[i][b, :, :L], mass[b, :, :L], room[2][b, :, :L])
+
+
+def evicted(cache, lengths, keep, recent):
+    """The definition of eviction on whole tensors: kept [B, Hk, keep], and for the kept
+    tokens codes (as values), scales and masses.  Values and scales are exact in fp32."""
+    m = cache.mass.double()
+    B, Hk, cap = m.shape
+    t = torch.arange(cap, device=m.device)
+    L = lengths.long().clamp(0, cap)
+    n = L.clamp(max=keep)
+    rec = n.clamp(max=recent)
+    older = (t < (L - rec)[:, None])[:, None].expand(B, Hk, cap)
+    # descending by mass among the older, NaN behind -inf, the lowest index first
+    rank = torch.where(older, torch.where(torch.isnan(m), 1, 0), 2)
+    order = torch.sort(torch.nan_to_num(m, nan=0.0, posinf=float("inf"), neginf=float("-inf")),
+                       dim=-1, descending=True, stable=True).indices
+    order = order.gather(-1, torch.sort(rank.gather(-1, order), dim=-1, stable=True).indices)
+    place = torch.empty_like(order).scatter_(-1, order, t.expand(B, Hk, cap))
+    stays = (older & (place < (n - rec)[:, None, None])) | (~older & (t < L[:, None])[:, None])
+    kept = torch.sort(torch.where(stays, t, t + cap), dim=-1).values[..., :keep]
+    kept = torch.where((torch.arange(keep, device=m.device) < n[:, None])[:, None], kept, -1)
+    pad = -keep % 32
+    src = torch.nn.functional.pad(kept, (0, pad), value=-1)
+    live, at = src >= 0, src.clamp(min=0)
+    same = ((src == torch.arange(keep + pad, device=m.device)) | ~live).view(B, Hk, -1, 32).all(-1)
+    out = {}
+    for name in ("k", "v"):
+        codes, scales = getattr(cache, name), getattr(cache, name + "_scale")
+        d = codes.shape[-1]
+        x = codes.view(torch.uint8).gather(2, at[..., None].expand(-1, -1, -1, d)).view(ref.E4M3).float()
+        x = torch.where(live[..., None], x * scales.gather(2, at // 32)[..., None], 0.0)
+        top, e = torch.frexp(x.view(B, Hk, -1, 32 * d).abs().amax(-1))
+        e = torch.where(top > 0.875, e - 8, e - 9)
+        s = torch.exp2(torch.where(top > 0, e, -40).clamp(-40, 40).float())
+        s = torch.where(same, scales[..., : s.shape[-1]], s)
+        code = (x / s.repeat_interleave(32, -1)[..., None]).clamp(-448.0, 448.0).to(ref.E4M3).float()
+        out[name] = (code, s)
+    return kept, n, live, out, torch.where(live, cache.mass.gather(2, at), 0.0)
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("B,Hk,cap,keep,recent", [
+    (1, 1, 65536, 30000, 100),      # 8 CTAs a head, 8 keys a thread
+    (1, 1, 131072, 777, 0),         # 16
+    (1, 1, 262144, 200000, 3000),   # 32
+    (1, 1, 300032, 100001, 77),     # more keys than a cluster holds
+    (20, 1, 20000, 5000, 40),       # 4 CTAs a head, 8 keys
+    (10, 4, 8192, 8000, 0),         # 2 CTAs a head
+    (38, 2, 2048, 1000, 7),         # one CTA a head, 2 keys
+    (19, 4, 7008, 3333, 50),        # 8
+    (16, 8, 16000, 15000, 16),      # 16
+    (25, 3, 30016, 1, 0),           # 32
+    (75, 1, 32768, 20000, 20000)])  # 32, mostly recent tokens
+def test_eviction_selections(rfb_lib, cuda_dev, in_place, B, Hk, cap, keep, recent):
+    """Every way the selection is laid out: few tokens a thread and many, one CTA a head and
+    clusters, masses with ties across their stretches, NaN, infinities and zeros of both signs."""
+    cache, _ = filled(rfb_lib, cuda_dev, B, Hk, cap, 32, 0, seed=cap + B, spread=2.0, mass=True)
+    g = gen(cap)
+    m = cache.mass
+    u = torch.rand(B, Hk, cap, generator=g).to(cuda_dev)
+    m[u < 0.3] = 0.25                       # a third of all ties
+    m[(u >= 0.3) & (u < 0.35)] = NAN
+    m[(u >= 0.35) & (u < 0.36)] = float("inf")
+    m[(u >= 0.36) & (u < 0.37)] = float("-inf")
+    m[(u >= 0.37) & (u < 0.38)] = -0.0
+    m[(u >= 0.38) & (u < 0.39)] = 0.0
+    m[(u >= 0.39) & (u < 0.40)] *= -1.0
+    if B * Hk > 2:
+        m[0, -1] = NAN                      # one value for a whole head
+        m[1, 0] = 0.5
+    L = [cap, cap - 1, cap // 2 + 5, 33, 0, 1, cap // 3, keep, keep + 1, cap // 7]
+    lengths = ints([L[b % len(L)] for b in range(B)], cuda_dev)
+    kept, n, live, want, mass = evicted(cache, lengths, keep, recent)
+    to = cache if in_place else rfb_lib.Cache8.create(B, Hk, keep, 32, mass=True, device=cuda_dev)
+    before = to.mass.clone()
+    got_n, got = rfb_lib.cache_evict(cache, lengths, keep, recent, out=None if in_place else to)
+    assert torch.equal(got_n.long(), n) and torch.equal(got.long(), kept)
+    rows = live.shape[-1]
+    for name, (code, s) in want.items():
+        c = getattr(to, name)[:, :, :rows].float()
+        assert torch.equal(c[live], code[live]), name
+        some = live.view(B, Hk, -1, 32).any(-1)
+        assert torch.equal(getattr(to, name + "_scale")[..., : rows // 32][some], s[some]), name
+    got_m = to.mass[..., :rows]
+    assert torch.equal(got_m[live].nan_to_num(77.0), mass[live].nan_to_num(77.0))
+    behind = torch.arange(to.cap, device=cuda_dev) >= n[:, None, None].expand(B, Hk, 1)
+    assert torch.equal(to.mass[behind].nan_to_num(77.0), before[behind].nan_to_num(77.0))
