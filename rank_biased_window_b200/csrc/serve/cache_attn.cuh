@@ -253,8 +253,8 @@ __device__ __forceinline__ float row_fragments(const uint2* raw, uint32_t (*frag
   }
   top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
   top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  // exponent held so that 2^(14 - e) and its inverse are normal
-  const int e = min(max(__float_as_int(top) >> 23, 60), 194) - 127;
+  // exponent held so that 2^(14 - e) and its inverse are normal: every one from 2^-112 up
+  const int e = min(max(__float_as_int(top) >> 23, 15), 254) - 127;
   const float to = pow2f(14 - e);
 #pragma unroll
   for (int i = 0; i < C / 16; ++i) {

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from tests import _serving_ref as ref
-from tests.test_gpu_serving import filled, gen, ints
+from tests.test_gpu_serving import filled, gen, ints, run_attn
 
 pytestmark = pytest.mark.gpu
 NAN = float("nan")
@@ -137,3 +137,14 @@ def test_eviction_selections(rfb_lib, cuda_dev, in_place, B, Hk, cap, keep, rece
     assert torch.equal(got_m[live].nan_to_num(77.0), mass[live].nan_to_num(77.0))
     behind = torch.arange(to.cap, device=cuda_dev) >= n[:, None, None].expand(B, Hk, 1)
     assert torch.equal(to.mass[behind].nan_to_num(77.0), before[behind].nan_to_num(77.0))
+
+
+@pytest.mark.parametrize("cap,L", [(128, 100), (4096, 4000)])
+@pytest.mark.parametrize("Nq", [1, 9])
+@pytest.mark.parametrize("power", [0, 60, 66, 67, 68, 80, 120, -60, -66, -68, -80, -100, -110])
+def test_attention_queries_of_any_size(rfb_lib, cuda_dev, power, Nq, cap, L):
+    """Queries around 2^power with a scale of 2^-power: ordinary scores, with weights."""
+    cache, refs = filled(rfb_lib, cuda_dev, 1, 1, cap, 64, 8, seed=41)
+    q = torch.randn(1, 4, Nq, 64, generator=gen(200 + power)) * 2.0 ** power
+    run_attn(rfb_lib, cuda_dev, cache, refs, [L], 4, Nq, q=q.bfloat16(), scale=2.0 ** -power,
+             mass=torch.zeros(1, 1, cap, device=cuda_dev))
