@@ -45,6 +45,9 @@ constexpr int kCaThreads = kCaWarps * 32;
 constexpr unsigned kCaSegmentCost = 4;
 constexpr float kCaLift = 11.f;   // weights are held as 2^(x - max + 11) ...
 constexpr float kCaSlack = 4.f;   // ... with a max that scores may pass by 2^4 before it moves
+// From here on (2^22, where fp32 steps by 1/2) neither: max - 11 would round to a multiple
+// of up to 16, and a weight past fp16's largest.
+constexpr float kCaCoarse = 4194304.f;
 
 struct CacheAttnArgs {
   const __nv_bfloat16* q;  // [B, Hk, R, d], R = group * Nq
@@ -711,10 +714,11 @@ __global__ void __launch_bounds__(kCaThreads, 3)
             for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
             al[e] = 1.f;
             if (v > over[q][e]) {
-              v -= kCaLift;
+              const bool fine = fabsf(v) < kCaCoarse;
+              v -= fine ? kCaLift : 0.f;
               al[e] = over[q][e] == -INFINITY ? 0.f : fast_exp2(m[q][e] - v);
               m[q][e] = v;
-              over[q][e] = v + (kCaLift + kCaSlack);
+              over[q][e] = v + (fine ? kCaLift + kCaSlack : 0.f);
             }
             l[q][e] *= al[e];
             al[e] *= back;

@@ -148,3 +148,17 @@ def test_attention_queries_of_any_size(rfb_lib, cuda_dev, power, Nq, cap, L):
     q = torch.randn(1, 4, Nq, 64, generator=gen(200 + power)) * 2.0 ** power
     run_attn(rfb_lib, cuda_dev, cache, refs, [L], 4, Nq, q=q.bfloat16(), scale=2.0 ** -power,
              mass=torch.zeros(1, 1, cap, device=cuda_dev))
+
+
+@pytest.mark.parametrize("cap,L", [(128, 100), (4096, 4000)])
+@pytest.mark.parametrize("Nq", [1, 9])
+@pytest.mark.parametrize("power", [10, 16, 19, 21, 22, 23, 24, 25, 26, 27, 28, 30, 45, 80])
+def test_attention_scores_of_any_size(rfb_lib, cuda_dev, power, Nq, cap, L):
+    """Scores around 2^power, each sign first: past 2^24 a score less a constant
+    rounds by more than the constant, and a weight may not leave fp16's range."""
+    cache, refs = filled(rfb_lib, cuda_dev, 1, 1, cap, 64, 8, seed=41)
+    q = torch.randn(1, 4, Nq, 64, generator=gen(power)) * 2.0 ** power
+    u = torch.zeros(1, 4, Nq, 8)
+    u[:, 1] = torch.randn(1, Nq, 8, generator=gen(power + 1)) * 2.0 ** power
+    q[:, 1] = 0.0
+    run_attn(rfb_lib, cuda_dev, cache, refs, [L], 4, Nq, q=q.bfloat16(), u=u.bfloat16())
