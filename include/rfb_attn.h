@@ -372,6 +372,11 @@ RFB_API int rfb_cache_append(const void* k, const void* v, const void* w, const 
  *       a row and token of capacity).
  * heads a multiple of heads_kv; made for steps of one to some dozens of tokens
  * (the cache is read once per 64 query rows of a key head).
+ * rfb_attn_fwd_cache_counts takes batches padded to Nq rows: counts, device int32
+ * [B] (clamped to [0, Nq]; NULL for Nq each), says that a sequence's queries are the
+ * first counts[b] rows of q and u, as append takes them, and with causal the last
+ * counts[b] of its lengths[b] tokens: row i sees t <= lengths[b] - counts[b] + i.  The
+ * rows behind them are not looked at: they get O = 0, LSE = -inf and add no weight.
  */
 RFB_API size_t rfb_attn_fwd_cache_workspace_size(int B, int heads, int heads_kv, int Nq, int cap,
                                                  int d, int with_mass);
@@ -381,6 +386,14 @@ RFB_API int rfb_attn_fwd_cache(const void* q, const void* u, const void* k8, con
                                float* mass_out, float decay, void* o, float* lse, void* workspace,
                                size_t workspace_bytes, int B, int heads, int heads_kv, int Nq,
                                int cap, int d, int r, float scale, int causal, void* stream);
+RFB_API int rfb_attn_fwd_cache_counts(const void* q, const void* u, const void* k8,
+                                      const void* v8, const void* w8, const float* k_scale,
+                                      const float* v_scale, const float* w_scale,
+                                      const int* lengths, const int* counts, const float* mass,
+                                      float* mass_out, float decay, void* o, float* lse,
+                                      void* workspace, size_t workspace_bytes, int B, int heads,
+                                      int heads_kv, int Nq, int cap, int d, int r, float scale,
+                                      int causal, void* stream);
 
 /*
  * Eviction by accumulated attention weight.  Per sequence and head, of L

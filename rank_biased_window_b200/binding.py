@@ -45,6 +45,8 @@ SIGNATURES = {
     "rfb_cache_append": (_i, [_vp] * 13 + [_i] * 6 + [_vp]),
     "rfb_attn_fwd_cache_workspace_size": (_sz, [_i] * 7),
     "rfb_attn_fwd_cache": (_i, [_vp] * 11 + [_f] + [_vp] * 3 + [_sz] + [_i] * 7 + [_f, _i, _vp]),
+    "rfb_attn_fwd_cache_counts": (_i, [_vp] * 12 + [_f] + [_vp] * 3 + [_sz] + [_i] * 7
+                                  + [_f, _i, _vp]),
     "rfb_cache_evict": (_i, [_vp] * 17 + [_i] * 8 + [_vp]),
     "rfb_strerror": (ctypes.c_char_p, [_i]),
     "rfb_last_device_error": (_i, []),

@@ -26,7 +26,7 @@ struct Api {
   decltype(&rfb_rotary) rotary = nullptr;
   decltype(&rfb_cache_append) append = nullptr;
   decltype(&rfb_attn_fwd_cache_workspace_size) workspace = nullptr;
-  decltype(&rfb_attn_fwd_cache) attn = nullptr;
+  decltype(&rfb_attn_fwd_cache_counts) attn = nullptr;
   decltype(&rfb_cache_evict) evict = nullptr;
   decltype(&rfb_strerror) strerror = nullptr;
   decltype(&rfb_last_cuda_error) cuda_error = nullptr;
@@ -307,7 +307,7 @@ PyObject* append(PyObject* const* a) {
   Py_RETURN_NONE;
 }
 
-// attn(cache, q, u, lengths, scale, causal, mass, mass_out, decay, out, lse, workspace)
+// attn(cache, q, u, lengths, scale, causal, mass, mass_out, decay, out, lse, workspace, counts=None)
 PyObject* attn(PyObject* const* a) {
   const Cache& c = cache_of(a[0]);
   const at::Device dev = c.device();
@@ -327,6 +327,12 @@ PyObject* attn(PyObject* const* a) {
     refuse(PyExc_ValueError, H, " query heads are not a multiple of the cache's ", c.Hk);
   const at::Tensor& lengths = tensor(a[3], "lengths");
   require("lengths", lengths, at::kInt, {c.B}, dev);
+  const int* counts = nullptr;
+  if (a[12] != Py_None) {
+    const at::Tensor& t = tensor(a[12], "counts");
+    require("counts", t, at::kInt, {c.B}, dev);
+    counts = static_cast<const int*>(t.const_data_ptr());
+  }
   const float* mass = nullptr;
   float* mass_out = nullptr;
   if (a[6] != Py_None) {
@@ -372,7 +378,7 @@ PyObject* attn(PyObject* const* a) {
   }
   const int rc = call(api.attn, q.const_data_ptr(), u, c.ptr(0), c.ptr(1), c.ptr(2), c.scale(0),
                       c.scale(1), c.scale(2), static_cast<const int*>(lengths.const_data_ptr()),
-                      mass, mass_out, decay, out.data_ptr(), static_cast<float*>(lse.data_ptr()),
+                      counts, mass, mass_out, decay, out.data_ptr(), static_cast<float*>(lse.data_ptr()),
                       ws.data_ptr(), ws.nbytes(), B, h, hk, nq, cap, d, static_cast<int>(c.r),
                       static_cast<float>(scale), causal, on.stream);
   if (rc == RFB_ERR_WORKSPACE)
@@ -420,12 +426,17 @@ PyObject* init(PyObject* const* a) {
   Py_RETURN_NONE;
 }
 
-// No C++ exception leaves an entry.
-template <PyObject* (*F)(PyObject* const*), int N>
+// No C++ exception leaves an entry.  The last MORE arguments may be left out (None).
+template <PyObject* (*F)(PyObject* const*), int N, int MORE>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  if (n != N) {
+  if (n < N || n > N + MORE) {
     PyErr_Format(PyExc_TypeError, "expected %d arguments, got %zd", N, n);
     return nullptr;
+  }
+  PyObject* all[N + MORE];
+  if (n < N + MORE) {
+    for (int i = 0; i < N + MORE; ++i) all[i] = i < n ? args[i] : Py_None;
+    args = all;
   }
   try {
     return F(args);
@@ -447,10 +458,11 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return nullptr;
 }
 
-#define RFB_ENTRY(NAME, N) \
-  {#NAME, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&entry<NAME, N>)), METH_FASTCALL, ""}
-PyMethodDef methods[] = {RFB_ENTRY(rotary, 9), RFB_ENTRY(cache, 6),  RFB_ENTRY(append, 7),
-                         RFB_ENTRY(attn, 12),  RFB_ENTRY(evict, 7),  RFB_ENTRY(init, 7),
+#define RFB_ENTRY(NAME, N, MORE)                                                                  \
+  {#NAME, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&entry<NAME, N, MORE>)), METH_FASTCALL, \
+   ""}
+PyMethodDef methods[] = {RFB_ENTRY(rotary, 9, 0), RFB_ENTRY(cache, 6, 0), RFB_ENTRY(append, 7, 0),
+                         RFB_ENTRY(attn, 12, 1),  RFB_ENTRY(evict, 7, 0), RFB_ENTRY(init, 7, 0),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_serving_bind", "", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

@@ -55,6 +55,7 @@ struct CacheAttnArgs {
   const uint8_t *k, *v, *w;
   const float *ks, *vs, *ws;
   const int* lengths;
+  const int* counts;  // [B] or null: the sequence's queries are the first counts[b] of Nq
   __nv_bfloat16* o;
   float* lse;
   float* scores;  // [B, Hk, R, cap] log2 scores for the mass, or null
@@ -78,6 +79,14 @@ struct CacheAttnArgs {
 
 __device__ __forceinline__ int cache_blocks(const CacheAttnArgs& a, int b) {
   return (min(max(a.lengths[b], 0), a.cap) + kCacheBlock - 1) / kCacheBlock;
+}
+// Whether queries of a sequence may see different tokens.
+__device__ __forceinline__ bool masked(const CacheAttnArgs& a) { return a.causal || a.counts; }
+// Tokens of the sequence's L that query row `row` sees; rows behind its own queries see none.
+__device__ __forceinline__ int row_sees(const CacheAttnArgs& a, int b, int row, int L) {
+  if (!masked(a) || row >= a.R) return L;
+  const int n = a.counts ? min(max(a.counts[b], 0), a.Nq) : a.Nq, i = row % a.Nq;
+  return i >= n ? 0 : a.causal ? max(min(L, L - n + 1 + i), 0) : L;
 }
 // Length on the line of a segment of n blocks: its cost, then its blocks; an
 // empty one has none.
@@ -364,7 +373,7 @@ __device__ __noinline__ void pv_edge_queries(const uint32_t (*p)[QT][2], uint32_
 }
 template <int D, int QT>
 __device__ __forceinline__ void pv_edge(const uint32_t (*p)[QT][2], uint32_t vrow, int tok0, int L,
-                                        const int (*lim)[2], int causal, float (*o)[QT][4]) {
+                                        const int (*lim)[2], bool masked, float (*o)[QT][4]) {
   constexpr int VW = D / 32;
   const int t = lane_id() & 3;
   uint32_t nan = 0;
@@ -378,7 +387,7 @@ __device__ __forceinline__ void pv_edge(const uint32_t (*p)[QT][2], uint32_t vro
       for (int w = 0; w < VW; ++w)
         if (tok0 + piece_token(kk, i, t) < L) nan |= __vcmpeq4(v[i][w] & 0x7f7f7f7fu, 0x7f7f7f7fu);
   }
-  if (causal && __any_sync(0xffffffffu, nan != 0)) {
+  if (masked && __any_sync(0xffffffffu, nan != 0)) {
     float c[D / 16][QT][4] = {};
     uint32_t pc[2][QT][2];
     int lc[QT][2];
@@ -555,8 +564,7 @@ __global__ void __launch_bounds__(kCaThreads, 3)
       const float f = row_fragments<D>(raw_q[q], qf[q]) * a.scale_log2;
       float e = 0.f;
       if constexpr (RP > 0) e = row_fragments<RP>(raw_u[q], uf[q]) * kLog2e;
-      int n = L;
-      if (a.causal && row < a.R) n = max(min(L, L - a.Nq + 1 + row % a.Nq), 0);
+      const int n = row_sees(a, b, row, L);
       lim_lo = min(lim_lo, n);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -753,7 +761,7 @@ __global__ void __launch_bounds__(kCaThreads, 3)
           pv_step<VW, QT>(p[kk], v, oacc);
         }
       } else {
-        pv_edge<D, QT>(p, vrow, blk * kCacheBlock, L, lim, a.causal, oacc);
+        pv_edge<D, QT>(p, vrow, blk * kCacheBlock, L, lim, masked(a), oacc);
       }
       held = st;
       __syncwarp();  // the stage has been read
@@ -1155,7 +1163,7 @@ __device__ __forceinline__ void recompute_mass(const CacheAttnArgs& a, unsigned 
         for (int k = 0; k < WW; ++k) su[q][k][lane] = make_uint2(uf[k][0], uf[k][1]);
       }
       // a row that is none weighs nothing (its LSE is +inf)
-      const int lim = a.causal && row < a.R ? max(min(L, L - a.Nq + 1 + row % a.Nq), 0) : L;
+      const int lim = row_sees(a, b, row, L);
       few = min(few, lim);
       if (t == 0) row_of[8 * q + g] = make_float4(f, e, 0.f, __int_as_float(lim));
     }

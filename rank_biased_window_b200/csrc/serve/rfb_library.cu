@@ -340,6 +340,18 @@ int rfb_attn_fwd_cache(const void* q, const void* u, const void* k8, const void*
                        float* lse, void* workspace, size_t workspace_bytes, int B, int heads,
                        int heads_kv, int Nq, int cap, int d, int r, float scale, int causal,
                        void* stream) {
+  return rfb_attn_fwd_cache_counts(q, u, k8, v8, w8, k_scale, v_scale, w_scale, lengths, nullptr,
+                                   mass, mass_out, decay, o, lse, workspace, workspace_bytes, B,
+                                   heads, heads_kv, Nq, cap, d, r, scale, causal, stream);
+}
+
+int rfb_attn_fwd_cache_counts(const void* q, const void* u, const void* k8, const void* v8,
+                              const void* w8, const float* k_scale, const float* v_scale,
+                              const float* w_scale, const int* lengths, const int* counts,
+                              const float* mass, float* mass_out, float decay, void* o, float* lse,
+                              void* workspace, size_t workspace_bytes, int B, int heads,
+                              int heads_kv, int Nq, int cap, int d, int r, float scale, int causal,
+                              void* stream) {
   if (heads < 0 || Nq < 0 || !std::isfinite(scale) || !(scale > 0.f) || !std::isfinite(decay))
     return RFB_ERR_INVALID_ARG;
   if (int rc = check_cache(B, heads_kv, cap, d, r)) return rc;
@@ -366,7 +378,8 @@ int rfb_attn_fwd_cache(const void* q, const void* u, const void* k8, const void*
     return RFB_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(u) || !aligned16(k8) || !aligned16(v8) || !aligned16(w8) ||
       !aligned16(o) || !aligned16(lse) || !aligned16(k_scale) || !aligned16(v_scale) ||
-      !aligned16(w_scale) || !aligned16(mass) || !aligned16(mass_out) || !aligned_to(lengths, 4))
+      !aligned16(w_scale) || !aligned16(mass) || !aligned16(mass_out) || !aligned_to(lengths, 4) ||
+      !aligned_to(counts, 4))
     return RFB_ERR_ALIGNMENT;
   DeviceInfo dev;
   if (int rc = current_device(&dev)) return rc;
@@ -383,6 +396,7 @@ int rfb_attn_fwd_cache(const void* q, const void* u, const void* k8, const void*
   a.w = static_cast<const uint8_t*>(w8);
   a.ks = k_scale, a.vs = v_scale, a.ws = w_scale;
   a.lengths = lengths;
+  a.counts = counts;
   a.o = static_cast<__nv_bfloat16*>(o);
   a.lse = lse;
   char* ws = static_cast<char*>(workspace);

@@ -40,7 +40,7 @@ def _load_bind():
         raise RuntimeError(f"the serving extension was built for torch {_serving_bind.torch_version} "
                            "(run `python -m rank_biased_window_b200.build --force`)")
     names = ("rfb_rotary", "rfb_cache_append", "rfb_attn_fwd_cache_workspace_size",
-             "rfb_attn_fwd_cache", "rfb_cache_evict", "rfb_strerror", "rfb_last_cuda_error")
+             "rfb_attn_fwd_cache_counts", "rfb_cache_evict", "rfb_strerror", "rfb_last_cuda_error")
     _serving_bind.init(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names))
     _bind = _serving_bind
     return _bind
@@ -278,15 +278,18 @@ def attn_cache_workspace_size(cache, heads, Nq, with_mass=False) -> int:
             cache.B, heads, cache.Hk, Nq, cache.cap, cache.d, 1 if with_mass else 0))
 
 
-def attn_fwd_cache(q, u, cache, lengths, scale=None, *, causal=True, mass=None, mass_out=None,
-                   decay=1.0, out=None, lse=None, workspace=None, stream=None):
+def attn_fwd_cache(q, u, cache, lengths, scale=None, *, causal=True, counts=None, mass=None,
+                   mass_out=None, decay=1.0, out=None, lse=None, workspace=None, stream=None):
     """O, LSE of Nq query tokens a sequence over the cached tokens, with the
     bias U W^T: q [B, H, Nq, d], u [B, H, Nq, r] (None when the cache holds no
     factors), H a multiple of the cache's heads, lengths int32 [B].
 
     causal: the queries are the last Nq of the lengths[b] tokens, and query i
     sees the tokens up to its own; otherwise every query sees all of them.  A
-    query without tokens gets O = 0 and LSE = -inf.  mass_out (fp32 [B, Hk,
+    query without tokens gets O = 0 and LSE = -inf.  counts (int32 [B]): a batch
+    padded to Nq rows, whose sequences have the first counts[b] of them, as
+    cache_append takes its rows; those are then the last counts[b] tokens, and
+    the rows behind them get O = 0, LSE = -inf and add no weight.  mass_out (fp32 [B, Hk,
     cap]) receives decay * mass + the softmax weights that each token got,
     summed over the queries of its head; it may be mass itself (cache.mass, to
     gather what cache_evict goes by), and mass None counts as zeros.  out must
@@ -294,7 +297,8 @@ def attn_fwd_cache(q, u, cache, lengths, scale=None, *, causal=True, mass=None, 
     """
     if not isinstance(cache, Cache8):
         raise TypeError("cache must be a Cache8")
-    args = (cache._tensors, q, u, lengths, scale, causal, mass, mass_out, decay, out, lse, workspace)
+    args = (cache._tensors, q, u, lengths, scale, causal, mass, mass_out, decay, out, lse, workspace,
+            counts)
     if stream is None:
         return _bind.attn(*args)
     return _on_stream(cache.device, stream, _bind.attn, *args)

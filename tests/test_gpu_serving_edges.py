@@ -162,3 +162,92 @@ def test_attention_scores_of_any_size(rfb_lib, cuda_dev, power, Nq, cap, L):
     u[:, 1] = torch.randn(1, Nq, 8, generator=gen(power + 1)) * 2.0 ** power
     q[:, 1] = 0.0
     run_attn(rfb_lib, cuda_dev, cache, refs, [L], 4, Nq, q=q.bfloat16(), u=u.bfloat16())
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("mass", [True, False])
+@pytest.mark.parametrize("H,Hk,Nq,cap,d,r", [
+    (2, 2, 5, 256, 64, 8),        # up to 8 rows, a CTA a segment
+    (1, 1, 7, 4096, 32, 0),       # the same, many CTAs
+    (4, 1, 40, 256, 64, 24),      # several row segments
+    (2, 1, 9, 2048, 128, 64),     # weights beside the join
+    (3, 1, 50, 4096, 64, 16)])    # weights behind it
+def test_attention_of_a_padded_batch(rfb_lib, cuda_dev, H, Hk, Nq, cap, d, r, mass, causal):
+    """Sequences with fewer queries than rows, appended and asked with the same counts:
+    each as if it were alone, whatever lies in the rows behind its queries."""
+    counts = [Nq, 1, Nq - 1, 0, Nq // 2, Nq + 3, -2]
+    lengths = [cap - 3, 33, Nq - 1, 60, cap // 2, Nq, 20]
+    B, g = len(counts), gen(cap + Nq)
+    cache, refs = filled(rfb_lib, cuda_dev, B, Hk, cap, d, r, seed=Nq)
+    n = [min(max(c, 0), Nq) for c in counts]
+    new = {m: torch.randn(B, Hk, Nq, ch, generator=g).bfloat16() if ch else None
+           for m, ch in (("k", d), ("v", d), ("w", r))}
+    begin = [L - c for L, c in zip(lengths, n)]
+    q = torch.randn(B, H, Nq, d, generator=g).bfloat16()
+    u = (torch.randn(B, H, Nq, r, generator=g) * r ** -0.5).bfloat16() if r else None
+    for b in range(B):      # what a padded batch holds there
+        for t in (q, u):
+            if t is not None:
+                t[b, :, n[b]:] = NAN if b % 2 else 3.0e38
+    c = ints(counts, cuda_dev)
+    rfb_lib.cache_append(cache, *(t if t is None else t.to(cuda_dev) for t in new.values()),
+                         start=ints(begin, cuda_dev), counts=c)
+    for m, rf in refs.items():
+        rf.append(new[m], begin, n)
+    old = torch.rand(B, Hk, cap, generator=g)
+    got_m = torch.full((B, Hk, cap), 123.0, device=cuda_dev)
+    kw = dict(mass=old.to(cuda_dev), mass_out=got_m, decay=0.5) if mass else {}
+    o, lse = rfb_lib.attn_fwd_cache(q.to(cuda_dev), u.to(cuda_dev) if r else None, cache,
+                                    ints(lengths, cuda_dev), causal=causal, counts=c, **kw)
+    val = {m: rf.values() for m, rf in refs.items()}
+    for b in range(B):
+        one = {m: v[b: b + 1] for m, v in val.items()}
+        qs, us = q[b: b + 1, :, : n[b]], u[b: b + 1, :, : n[b]] if r else None
+        ro, rl, rm, room = ref.attention(qs, us, one["k"], one["v"], one.get("w"), [lengths[b]],
+                                         d ** -0.5, causal, old[b: b + 1], 0.5)
+        ref.assert_within(f"o {b}", o[b: b + 1, :, : n[b]], ro, room[0])
+        ref.assert_within(f"lse {b}", lse[b: b + 1, :, : n[b]], rl, room[1])
+        assert bool((o[b, :, n[b]:] == 0).all()) and bool((lse[b, :, n[b]:] == float("-inf")).all())
+        if mass:
+            L = lengths[b]
+            ref.assert_within(f"mass {b}", got_m[b: b + 1, :, :L], rm[:, :, :L], room[2][:, :, :L])
+            assert bool((got_m[b, :, L:] == 123.0).all())
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_padded_batch_with_nan_values(rfb_lib, cuda_dev, causal):
+    """A NaN value reaches the queries that see its token and no padding row; full counts
+    are the call without them, bit for bit."""
+    cache, _ = filled(rfb_lib, cuda_dev, 2, 1, 96, 64, 0, seed=61)
+    cache.v.view(torch.uint8)[:, 0, 40, 5] = 0x7f
+    q = torch.randn(2, 2, 12, 64, generator=gen(62)).bfloat16().to(cuda_dev)
+    L = ints([75, 42], cuda_dev)
+    o, lse = rfb_lib.attn_fwd_cache(q, None, cache, L, causal=causal, counts=ints([12, 4], cuda_dev))
+    assert bool(torch.isnan(o[0, :, :, 5]).all()) and not bool(torch.isnan(o[..., 6]).any())
+    sees = torch.tensor([40 <= 42 - 4 + i if causal else True for i in range(4)])
+    assert torch.equal(torch.isnan(o[1, 0, :4, 5]).cpu(), sees)
+    assert bool((o[1, :, 4:] == 0).all()) and bool((lse[1, :, 4:] == float("-inf")).all())
+    cache.v.view(torch.uint8)[:, 0, 40, 5] = 0
+    a = rfb_lib.attn_fwd_cache(q, None, cache, L, causal=causal)
+    b = rfb_lib.attn_fwd_cache(q, None, cache, L, causal=causal, counts=ints([12, 12], cuda_dev))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_counts_are_read_on_the_device_and_checked(rfb_lib, cuda_dev):
+    cache, _ = filled(rfb_lib, cuda_dev, 2, 2, 64, 64, 0, seed=7)
+    q = torch.randn(2, 4, 3, 64, generator=gen(8)).bfloat16().to(cuda_dev)
+    L, c = ints([9, 30], cuda_dev), ints([3, 1], cuda_dev)
+    for bad, err in ((c.long(), TypeError), (c[:1], ValueError), (c.cpu(), ValueError), (3, TypeError)):
+        with pytest.raises(err, match="counts"):
+            rfb_lib.attn_fwd_cache(q, None, cache, L, counts=bad)
+    rfb_lib.attn_fwd_cache(q, None, cache, L, counts=c)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = rfb_lib.attn_fwd_cache(q, None, cache, L, counts=c)
+    for v in ([3, 1], [0, 2], [1, 3]):
+        c.copy_(torch.tensor(v))
+        graph.replay()
+        eo, el = rfb_lib.attn_fwd_cache(q, None, cache, L, counts=c)
+        assert torch.equal(o, eo) and torch.equal(lse, el)
+        assert bool((lse[0, :, v[0]:] == float("-inf")).all()) and bool((lse[0, :, : v[0]] > -1e9).all())

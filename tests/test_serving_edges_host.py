@@ -76,3 +76,18 @@ def test_eviction_walk_names_only_what_exists(tmp_path):
     subprocess.run([build._nvcc(), *build.ARCH, "-std=c++17", "--expt-relaxed-constexpr", "-I", build.CSRC,
                     "-o", str(exe), str(src)], check=True, capture_output=True)
     assert subprocess.run([str(exe)], capture_output=True, text=True).stdout == "0\n"
+
+
+def test_attention_with_counts_host_checks(rfb_lib):
+    """The padded form checks as the plain one does, and has the plain one's arguments but one."""
+    lib = rfb_lib.load_library()
+
+    def call(B=1, H=2, Hk=1, Nq=1, cap=64, d=64, r=0, scale=0.1):
+        return lib.rfb_attn_fwd_cache_counts(*([None] * 12), 1.0, None, None, None, 0, B, H, Hk, Nq,
+                                             cap, d, r, scale, 1, None)
+    assert call(B=0) == 0 and call(Nq=0) == 0 and call(H=0) == 0
+    assert call() == 1 and call(scale=0.0) == 1 and call(H=3, Hk=2) == 1
+    assert call(d=96) == 2 and call(r=12) == 2 and call(cap=33) == 2
+    from rank_biased_window_b200.binding import SIGNATURES
+    plain, padded = (SIGNATURES["rfb_attn_fwd_cache" + s][1] for s in ("", "_counts"))
+    assert plain == padded[:9] + padded[10:]
