@@ -236,16 +236,35 @@ PyObject* rotary(PyObject* const* a) {
 struct Cache {
   at::Tensor t[6];  // k, v, w, their scales; w and its scale may be undefined
   int64_t B, Hk, cap, d, r;
+  at::Device on{at::kCPU};
+  // What a tensor was at the start it may no longer be (resize_, set_, .data, a freed storage).
+  bool as_made(int i) const {
+    const at::Tensor& x = t[i];
+    if (!x.defined()) return true;
+    const int64_t c = i < 2 ? d : r;
+    return (i < 3 ? x.sizes() == at::IntArrayRef({B, Hk, cap, c})
+                  : x.sizes() == at::IntArrayRef({B, Hk, cap / 32})) &&
+           x.is_contiguous() && x.device() == on &&
+           x.scalar_type() == (i < 3 ? at::kFloat8_e4m3fn : at::kFloat) &&
+           x.storage().nbytes() >= (x.storage_offset() + x.numel()) * x.element_size();
+  }
   void* ptr(int i) const { return t[i].defined() ? t[i].data_ptr() : nullptr; }
   float* scale(int i) const { return static_cast<float*>(ptr(3 + i)); }
-  at::Device device() const { return t[0].device(); }
+  at::Device device() const { return on; }
 };
 constexpr const char* kCacheName = "rank_biased_window_b200.Cache8";
+
+constexpr const char* kPart[6] = {"k", "v", "w", "k_scale", "v_scale", "w_scale"};
 
 Cache& cache_of(PyObject* o) {
   void* p = PyCapsule_GetPointer(o, kCacheName);
   if (!p) throw python_error();
-  return *static_cast<Cache*>(p);
+  Cache& c = *static_cast<Cache*>(p);
+  for (int i = 0; i < 6; ++i)
+    if (!c.as_made(i))
+      refuse(PyExc_ValueError, "the cache's ", kPart[i],
+             " is not what it was when the cache was made (size, layout, type, device or storage)");
+  return c;
 }
 
 // cache(k, v, w, k_scale, v_scale, w_scale): checked by the caller.
@@ -255,6 +274,7 @@ PyObject* cache(PyObject* const* a) {
     if (a[i] != Py_None) c->t[i] = THPVariable_Unpack(a[i]);
   c->B = c->t[0].size(0), c->Hk = c->t[0].size(1), c->cap = c->t[0].size(2), c->d = c->t[0].size(3);
   c->r = c->t[2].defined() ? c->t[2].size(3) : 0;
+  c->on = c->t[0].device();
   return PyCapsule_New(c, kCacheName, [](PyObject* o) {
     delete static_cast<Cache*>(PyCapsule_GetPointer(o, kCacheName));
   });

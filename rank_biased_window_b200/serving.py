@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import operator
 
 import torch
 
@@ -186,18 +187,29 @@ def rfb_rotary(q, k, positions, freqs, layout="half", amplitude=1.0):
 
 
 # -------------------------------------------------------------------- cache
+def _held(name):
+    """A tensor or size that a cache is made of.  The calls hold the tensors themselves, so
+    another one in its place would be read by some and not by others."""
+    def refuse(self, _):
+        raise AttributeError(f"a Cache8 keeps the {name} it was made with: write into the tensors, "
+                             "or make a new Cache8")
+    return property(operator.attrgetter("_" + name), refuse)
+
+
 class Cache8:
     """Keys, values and key factors of B sequences in 8 bits.
 
     k, v: e4m3 [B, Hk, cap, d]; w: e4m3 [B, Hk, cap, r] or None; k_scale,
     v_scale, w_scale: fp32 [B, Hk, cap / 32], one power of two per head and 32
     tokens; mass: fp32 [B, Hk, cap], the attention weight that each token
-    gathered, or None.  The object holds the tensors; how many tokens a sequence has is the caller's (int32 [B] on the device), one
-    for all layers of a model.
+    gathered, or None.  The object holds the tensors, whose contents may be
+    written but which cannot be exchanged (the mass can); how many tokens a
+    sequence has is the caller's (int32 [B] on the device), one for all layers
+    of a model.
     """
 
-    __slots__ = ("k", "v", "w", "k_scale", "v_scale", "w_scale", "mass", "device", "B", "Hk", "cap",
-                 "d", "r", "_tensors")
+    _FIXED = ("k", "v", "w", "k_scale", "v_scale", "w_scale", "device", "B", "Hk", "cap", "d", "r")
+    __slots__ = ("mass", "_tensors", *("_" + name for name in _FIXED))
 
     def __init__(self, k, v, w, k_scale, v_scale, w_scale, mass=None):
         dev = _cuda("k", k)
@@ -221,10 +233,9 @@ class Cache8:
                 _require(name, t, torch.float32, (B, Hk, cap // CACHE_BLOCK), dev)
         if mass is not None:
             _require("mass", mass, torch.float32, (B, Hk, cap), dev)
-        self.k, self.v, self.w = k, v, w
-        self.k_scale, self.v_scale, self.w_scale = k_scale, v_scale, w_scale
-        self.mass, self.device = mass, dev
-        self.B, self.Hk, self.cap, self.d, self.r = B, Hk, cap, d, r
+        self.mass = mass
+        for name, x in zip(self._FIXED, (k, v, w, k_scale, v_scale, w_scale, dev, B, Hk, cap, d, r)):
+            setattr(self, "_" + name, x)
         self._tensors = (_bind or _load_bind()).cache(k, v, w, k_scale, v_scale, w_scale)
 
     def __reduce__(self):  # copy and pickle
@@ -251,6 +262,11 @@ class Cache8:
         """The values that the codes of "k", "v" or "w" stand for, fp32."""
         codes, scales = getattr(self, name), getattr(self, name + "_scale")
         return codes.float() * scales.repeat_interleave(CACHE_BLOCK, dim=2)[..., None]
+
+
+for _name in Cache8._FIXED:
+    setattr(Cache8, _name, _held(_name))
+del _name
 
 
 def cache_append(cache, k, v, w=None, *, start, counts=None, stream=None):

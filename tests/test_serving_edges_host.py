@@ -91,3 +91,45 @@ def test_attention_with_counts_host_checks(rfb_lib):
     from rank_biased_window_b200.binding import SIGNATURES
     plain, padded = (SIGNATURES["rfb_attn_fwd_cache" + s][1] for s in ("", "_counts"))
     assert plain == padded[:9] + padded[10:]
+
+
+def _host_cache(bind):
+    c = [torch.zeros(2, 2, 64, ch, dtype=torch.uint8).view(torch.float8_e4m3fn) for ch in (64, 64, 8)]
+    s = [torch.ones(2, 2, 2) for _ in range(3)]
+    return bind.cache(*c, *s), c + s
+
+
+@pytest.mark.parametrize("part", ["k", "v", "w", "k_scale", "v_scale", "w_scale"])
+def test_cache_tensors_cannot_be_exchanged(part):
+    """The calls hold the tensors that a cache was made of: another one in an attribute's
+    place would be read by some of them only."""
+    from rank_biased_window_b200 import Cache8
+    c = object.__new__(Cache8)
+    for name in (part, "cap", "device"):
+        with pytest.raises(AttributeError, match="make a new Cache8"):
+            setattr(c, name, torch.zeros(1))
+    c.mass = None                   # looked at in each call
+
+
+@pytest.mark.parametrize("change", [
+    lambda t: t.resize_(2, 2, *[max(1, n // 2) for n in t.shape[2:]]),
+    lambda t: t.set_(torch.zeros(1, dtype=t.dtype).expand(t.shape)),
+    lambda t: setattr(t, "data", t.transpose(0, 1)),
+    lambda t: setattr(t, "data", t.double().to(torch.float16)),
+    lambda t: t.untyped_storage().resize_(0)])
+@pytest.mark.parametrize("part", range(6))
+def test_changed_cache_tensors_are_refused(rfb_lib, part, change):
+    """A held tensor that was resized, freed or pointed elsewhere in place: its sizes are
+    the cache's no longer, so no call may run with them."""
+    from rank_biased_window_b200 import serving
+    bind = serving._load_bind()
+    held, tensors = _host_cache(bind)
+    q = torch.zeros(2, 2, 1, 64, dtype=torch.bfloat16)
+    n = torch.zeros(2, dtype=torch.int32)
+    change(tensors[part])
+    name = ("k", "v", "w", "k_scale", "v_scale", "w_scale")[part]
+    for call in (lambda: bind.attn(held, q, q[..., :8], n, None, True, None, None, 1.0, None, None, None),
+                 lambda: bind.append(held, None, q, q, q[..., :8], n, None),
+                 lambda: bind.evict(held, None, held, None, n, 8, 0)):
+        with pytest.raises(ValueError, match=f"the cache's {name} is not what it was"):
+            call()
