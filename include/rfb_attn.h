@@ -370,6 +370,8 @@ RFB_API int rfb_cache_append(const void* k, const void* v, const void* w, const 
  *       rfb_attn_fwd_cache_workspace_size() bytes, as for rfb_attn_bwd (with
  *       mass_out and up to 8 query rows a key head it holds their scores, 4 bytes
  *       a row and token of capacity).
+ * o, lse, mass_out and workspace share no memory with one another or with an input,
+ * but for mass_out with mass.
  * heads a multiple of heads_kv; made for steps of one to some dozens of tokens
  * (the cache is read once per 64 query rows of a key head).
  * rfb_attn_fwd_cache_counts takes batches padded to Nq rows: counts, device int32
@@ -403,7 +405,8 @@ RFB_API int rfb_attn_fwd_cache_counts(const void* q, const void* u, const void* 
  * their mass.  A block of 32 whose tokens all stay where they are keeps its
  * codes and scale; every other block gets the scale of its own values.
  *   *_out : the cache that receives them, of capacity cap_out >= keep: all the
- *           same pointers as the inputs (in place), or none of them.
+ *           same pointers as the inputs (in place), or none of them and all of
+ *           it in memory of its own.
  *   new_lengths : int32 [B], written: n (not the lengths array itself).
  *   kept  : int32 [B, heads_kv, keep], written: the tokens' former positions,
  *           -1 behind the last.

@@ -93,10 +93,22 @@ bool meet(const at::Tensor& x, const at::Tensor& y) {
 void apart(const char* name, const at::Tensor& x, const char* other, const at::Tensor& y) {
   if (meet(x, y)) refuse(PyExc_ValueError, name, " must not share memory with ", other);
 }
-// In place or apart.
-void same_or_apart(const char* name, const at::Tensor& x, const char* other, const at::Tensor& y) {
-  if (x.const_data_ptr() != y.const_data_ptr()) apart(name, x, other, y);
-}
+// The memory of a contiguous tensor.
+struct Span {
+  const char* name;
+  const char *lo, *hi;
+  Span(const char* n, const at::Tensor& t)
+      : name(n), lo(t.defined() ? static_cast<const char*>(t.const_data_ptr()) : nullptr),
+        hi(t.defined() ? lo + t.numel() * t.element_size() : nullptr) {}
+  bool meets(const Span& o) const { return lo < hi && o.lo < o.hi && lo < o.hi && o.lo < hi; }
+  void apart(const Span& o) const {
+    if (meets(o)) refuse(PyExc_ValueError, name, " must not share memory with ", o.name);
+  }
+  // In place or apart.
+  void same_or_apart(const Span& o) const {
+    if (lo != o.lo) apart(o);
+  }
+};
 
 void check(int rc, const char* what) {
   if (rc == RFB_OK) return;
@@ -208,6 +220,8 @@ PyObject* rotary(PyObject* const* a) {
     require("q_out", qo, dt, q.sizes(), dev);
     apart("q_out", qo, "q", q);
     if (has_k) apart("q_out", qo, "k", k);
+    apart("q_out", qo, "positions", pos);
+    apart("q_out", qo, "freqs", freqs);
   }
   if (has_k) {
     if (a[8] == Py_None) {
@@ -218,6 +232,8 @@ PyObject* rotary(PyObject* const* a) {
       apart("k_out", ko, "q", q);
       apart("k_out", ko, "k", k);
       apart("k_out", ko, "q_out", qo);
+      apart("k_out", ko, "positions", pos);
+      apart("k_out", ko, "freqs", freqs);
     }
   }
   check(call(api.rotary, q.const_data_ptr(), has_k ? k.const_data_ptr() : nullptr, qo.data_ptr(),
@@ -232,11 +248,20 @@ PyObject* rotary(PyObject* const* a) {
   return pair(qo, has_k ? THPVariable_Wrap(ko) : Py_None);
 }
 
+constexpr const char* kPart[6] = {"the cache's k",       "the cache's v",       "the cache's w",
+                                  "the cache's k_scale", "the cache's v_scale", "the cache's w_scale"};
 // A cache's tensors, kept alive, with their sizes.
 struct Cache {
   at::Tensor t[6];  // k, v, w, their scales; w and its scale may be undefined
   int64_t B, Hk, cap, d, r;
   at::Device on{at::kCPU};
+  Span span(int i) const { return Span(kPart[i], t[i]); }
+  // For the calls that write the tensors: none may lie in another's memory or in the mass's.
+  void own_memory(const Span& mass) const {
+    const Span all[7] = {span(0), span(1), span(2), span(3), span(4), span(5), mass};
+    for (int i = 0; i < 7; ++i)
+      for (int k = 0; k < i; ++k) all[i].apart(all[k]);
+  }
   // What a tensor was at the start it may no longer be (resize_, set_, .data, a freed storage).
   bool as_made(int i) const {
     const at::Tensor& x = t[i];
@@ -254,15 +279,13 @@ struct Cache {
 };
 constexpr const char* kCacheName = "rank_biased_window_b200.Cache8";
 
-constexpr const char* kPart[6] = {"k", "v", "w", "k_scale", "v_scale", "w_scale"};
-
 Cache& cache_of(PyObject* o) {
   void* p = PyCapsule_GetPointer(o, kCacheName);
   if (!p) throw python_error();
   Cache& c = *static_cast<Cache*>(p);
   for (int i = 0; i < 6; ++i)
     if (!c.as_made(i))
-      refuse(PyExc_ValueError, "the cache's ", kPart[i],
+      refuse(PyExc_ValueError, kPart[i],
              " is not what it was when the cache was made (size, layout, type, device or storage)");
   return c;
 }
@@ -316,7 +339,9 @@ PyObject* append(PyObject* const* a) {
     require("counts", t, at::kInt, {c.B}, dev);
     counts = static_cast<const int*>(t.const_data_ptr());
   }
-  float* mass = a[1] == Py_None ? nullptr : floats(mass_of(a[1], c));
+  const at::Tensor kept = a[1] == Py_None ? at::Tensor() : mass_of(a[1], c);
+  c.own_memory(Span("the cache's mass", kept));
+  float* mass = kept.defined() ? floats(kept) : nullptr;
   Launch on(dev);
   check(call(api.append, x[0].const_data_ptr(), x[1].const_data_ptr(),
              c.r ? x[2].const_data_ptr() : nullptr, strides, c.ptr(0), c.ptr(1), c.ptr(2), c.scale(0),
@@ -364,7 +389,6 @@ PyObject* attn(PyObject* const* a) {
     const at::Tensor& t = tensor(a[7], "mass_out");
     require("mass_out", t, at::kFloat, {c.B, c.Hk, c.cap}, dev);
     mass_out = floats(t);
-    if (mass) same_or_apart("mass_out", t, "mass", mass_of(a[6], c));
   }
   const double scale = a[4] == Py_None ? 1.0 / std::sqrt(static_cast<double>(c.d)) : number(a[4]);
   const float decay = static_cast<float>(number(a[8]));
@@ -372,30 +396,39 @@ PyObject* attn(PyObject* const* a) {
   if (causal < 0) throw python_error();
   const int B = small(c.B, "B"), h = small(H, "H"), hk = small(c.Hk, "Hk"), nq = small(Nq, "Nq"),
             cap = small(c.cap, "capacity"), d = static_cast<int>(c.d);
-  Launch on(dev);
   at::Tensor out, lse, ws;
-  if (a[9] == Py_None) {
-    out = make(q.sizes(), at::kBFloat16, dev);
-  } else {
+  if (a[9] != Py_None) {
     out = tensor(a[9], "out");
     require("out", out, at::kBFloat16, q.sizes(), dev);
-    apart("out", out, "q", q);
-    if (u) apart("out", out, "u", THPVariable_Unpack(a[2]));
   }
-  if (a[10] == Py_None) {
-    lse = make({c.B, H, Nq}, at::kFloat, dev);
-  } else {
+  if (a[10] != Py_None) {
     lse = tensor(a[10], "lse");
     require("lse", lse, at::kFloat, {c.B, H, Nq}, dev);
   }
-  const size_t need = api.workspace(B, h, hk, nq, cap, d, mass_out != nullptr);
-  if (a[11] == Py_None) {
-    ws = make({static_cast<int64_t>(need) + 16}, at::kByte, dev);
-  } else {
+  if (a[11] != Py_None) {
     ws = tensor(a[11], "workspace");
     if (ws.device() != dev || !ws.is_contiguous())
       refuse(PyExc_ValueError, "workspace must be a contiguous tensor on ", device_text(dev));
   }
+  // what is written, of the caller's: apart from what is read and from one another
+  const auto given = [&](int i) { return a[i] == Py_None ? at::Tensor() : THPVariable_Unpack(a[i]); };
+  const Span written[4] = {{"out", out}, {"lse", lse}, {"workspace", ws}, {"mass_out", given(7)}};
+  const Span read[4] = {{"q", q}, {"u", given(2)}, {"lengths", lengths}, {"counts", given(12)}};
+  const Span mass_in("mass", given(6));
+  for (int i = 0; i < 4; ++i) {
+    const Span& x = written[i];
+    if (x.lo == x.hi) continue;
+    for (int k = 0; k < i; ++k) x.apart(written[k]);
+    for (const Span& y : read) x.apart(y);
+    for (int k = 0; k < 6; ++k) x.apart(c.span(k));
+    if (i < 3) x.apart(mass_in);
+    else x.same_or_apart(mass_in);
+  }
+  Launch on(dev);
+  if (!out.defined()) out = make(q.sizes(), at::kBFloat16, dev);
+  if (!lse.defined()) lse = make({c.B, H, Nq}, at::kFloat, dev);
+  const size_t need = api.workspace(B, h, hk, nq, cap, d, mass_out != nullptr);
+  if (!ws.defined()) ws = make({static_cast<int64_t>(need) + 16}, at::kByte, dev);
   const int rc = call(api.attn, q.const_data_ptr(), u, c.ptr(0), c.ptr(1), c.ptr(2), c.scale(0),
                       c.scale(1), c.scale(2), static_cast<const int*>(lengths.const_data_ptr()),
                       counts, mass, mass_out, decay, out.data_ptr(), static_cast<float*>(lse.data_ptr()),
@@ -412,13 +445,18 @@ PyObject* evict(PyObject* const* a) {
   const Cache &c = cache_of(a[0]), &to = cache_of(a[2]);
   const at::Device dev = c.device();
   const at::Tensor &mass = mass_of(a[1], c), &to_mass = mass_of(a[3], to);
-  if (&c != &to) {
-    for (int i = 0; i < 6; ++i)
-      if (c.t[i].defined()) same_or_apart("out", to.t[i], "the cache", c.t[i]);
-    same_or_apart("out", to_mass, "the cache", mass);
-  }
   const at::Tensor& lengths = tensor(a[4], "lengths");
   require("lengths", lengths, at::kInt, {c.B}, dev);
+  // each tensor in the place of its own kind or in no other's
+  to.own_memory(Span("the cache's mass", to_mass));
+  if (&c != &to) {
+    Span from[7] = {c.span(0), c.span(1), c.span(2), c.span(3), c.span(4), c.span(5), {"", mass}};
+    Span into[7] = {to.span(0), to.span(1), to.span(2), to.span(3), to.span(4), to.span(5), {"", to_mass}};
+    for (int i = 0; i < 7; ++i) {
+      into[i].name = "out", from[i].name = "the cache";
+      for (int k = 0; k < 7; ++k) i == k ? into[i].same_or_apart(from[k]) : into[i].apart(from[k]);
+    }
+  }
   const int keep = small(integer(a[5]), "keep"), recent = small(integer(a[6]), "recent");
   Launch on(dev);
   at::Tensor n = make({c.B}, at::kInt, dev);

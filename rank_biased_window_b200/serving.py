@@ -308,8 +308,9 @@ def attn_fwd_cache(q, u, cache, lengths, scale=None, *, causal=True, counts=None
     the rows behind them get O = 0, LSE = -inf and add no weight.  mass_out (fp32 [B, Hk,
     cap]) receives decay * mass + the softmax weights that each token got,
     summed over the queries of its head; it may be mass itself (cache.mass, to
-    gather what cache_evict goes by), and mass None counts as zeros.  out must
-    not share memory with q or u.
+    gather what cache_evict goes by), and mass None counts as zeros.  out, lse,
+    mass_out and workspace must not share memory with one another or with
+    anything that is read.
     """
     if not isinstance(cache, Cache8):
         raise TypeError("cache must be a Cache8")
@@ -325,8 +326,8 @@ def cache_evict(cache, lengths, keep, recent=0, *, out=None, stream=None):
     weight (cache.mass): the last `recent` tokens stay, and of those before
     them the ones with the largest mass, head by head, in their order.
 
-    The kept tokens move to the front of the cache, or of `out` (a Cache8 of
-    its own with the same heads and channels, of capacity >= keep).  Returns
+    The kept tokens move to the front of the cache, or of `out` (a Cache8 in
+    memory of its own with the same heads and channels, of capacity >= keep).  Returns
     the new lengths (int32 [B]) and the tokens' former positions (int32 [B,
     Hk, keep], -1 behind the last).
     """

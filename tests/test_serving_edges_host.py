@@ -133,3 +133,51 @@ def test_changed_cache_tensors_are_refused(rfb_lib, part, change):
                  lambda: bind.evict(held, None, held, None, n, 8, 0)):
         with pytest.raises(ValueError, match=f"the cache's {name} is not what it was"):
             call()
+
+
+def test_written_memory_is_apart(rfb_lib):
+    """What a call writes lies in nothing that it reads or writes besides, in whatever role;
+    refused before any launch."""
+    from rank_biased_window_b200 import serving
+    bind = serving._load_bind()
+    held, (k, v, w, ks, vs, ws) = _host_cache(bind)
+    q, u = torch.zeros(2, 4, 3, 64, dtype=torch.bfloat16), torch.zeros(2, 4, 3, 8, dtype=torch.bfloat16)
+    n, cnt = torch.zeros(2, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    mass = torch.zeros(2, 2, 64)
+    room = torch.zeros(1 << 16, dtype=torch.uint8)
+
+    def part(dtype, shape, at=0):
+        size = torch.empty(0, dtype=dtype).element_size() * torch.Size(shape).numel()
+        return room[at: at + size].view(dtype).view(shape)
+
+    def attn(**kw):
+        a = dict(mass=None, mass_out=None, out=None, lse=None, workspace=None, counts=cnt)
+        a.update(kw)
+        return bind.attn(held, q, u, n, None, True, a["mass"], a["mass_out"], 1.0, a["out"], a["lse"],
+                         a["workspace"], a["counts"])
+    lse = part(torch.float32, (2, 4, 3))
+    calls = [
+        (lambda: attn(out=part(torch.bfloat16, q.shape), lse=lse), "lse .* out"),
+        (lambda: attn(lse=lse, workspace=room), "workspace .* lse"),
+        (lambda: attn(lse=lse, mass_out=part(torch.float32, mass.shape, 64)), "mass_out .* lse"),
+        (lambda: attn(workspace=q), "workspace .* q"),
+        (lambda: attn(workspace=u), "workspace .* u"),
+        (lambda: attn(workspace=n), "workspace .* lengths"),
+        (lambda: attn(workspace=cnt), "workspace .* counts"),
+        (lambda: attn(workspace=mass, mass=mass, mass_out=mass), "workspace .* mass"),
+        (lambda: attn(lse=ks.view(-1)[:0].new_zeros(2, 4, 3), workspace=vs), "workspace .* the cache's v_scale"),
+        (lambda: attn(workspace=k), "workspace .* the cache's k"),
+        (lambda: attn(out=q), "out .* q")]
+    # a cache whose k and v exchange places, or that lies in one tensor twice
+    swapped, twice = bind.cache(v, k, w, vs, ks, ws), bind.cache(k, k, w, ks, vs, ws)
+    x = torch.zeros(2, 2, 1, 64, dtype=torch.bfloat16)
+    new = torch.zeros(2, 2, 64)
+    calls += [
+        (lambda: bind.evict(held, mass, swapped, new, n, 8, 0), "out .* the cache"),
+        (lambda: bind.evict(twice, mass, twice, mass, n, 8, 0), "the cache's v .* the cache's k"),
+        (lambda: bind.append(twice, mass, x, x, x[..., :8], n, None), "the cache's v .* the cache's k"),
+        (lambda: bind.append(held, k.view(-1)[: 4 * new.numel()].view(torch.float32).view(new.shape), x, x,
+                             x[..., :8], n, None), "the cache's mass .* the cache's k")]
+    for call, match in calls:
+        with pytest.raises(ValueError, match=match.replace(" .* ", " must not share memory with ")):
+            call()
