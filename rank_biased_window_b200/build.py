@@ -6,8 +6,11 @@ the serving calls' Python extension ``_serving_bind.so`` with the host compiler.
 The library is a plain C-ABI shared object (see include/rfb_attn.h); the
 Python binding loads it with ctypes.  The CUDA runtime is linked statically and
 the driver's tensor-map encoder is fetched at run time, so the .so depends on
-nothing but the NVIDIA driver.  The extension holds host code only and belongs
-to the Python and torch that it was built with.
+nothing but the NVIDIA driver, and nvcc is all that building it takes.  The
+extension holds host code only and belongs to the Python and torch that it was
+built with (which its stamp file names); it needs their headers.  Where it
+cannot be built the library is there all the same, and the serving calls say
+that they are not.
 """
 from __future__ import annotations
 
@@ -25,6 +28,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "librfb_attn.so")
 BIND = os.path.join(PKG, "_serving_bind.so")
+BIND_STAMP = os.path.join(PKG, "_serving_bind.stamp")
 BIND_SOURCE = os.path.join(CSRC, "serve", "bind.cpp")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -53,8 +57,25 @@ def up_to_date() -> bool:
     return _newer(LIB, sources())
 
 
+def _bind_of_these_sources() -> bool:
+    return _newer(BIND, [BIND_SOURCE, *glob.glob(os.path.join(INCLUDE, "*.h"))])
+
+
+def _bind_stamp() -> str:
+    import torch
+    return f"torch {torch.__version__} {sys.implementation.cache_tag}"
+
+
+def bind_up_to_date() -> bool:
+    """Built from these sources, for this Python and torch."""
+    if not (_bind_of_these_sources() and os.path.exists(BIND_STAMP)):
+        return False
+    with open(BIND_STAMP) as f:
+        return f.read() == _bind_stamp()
+
+
 def build_bind(force: bool = False) -> str:
-    if not force and _newer(BIND, [BIND_SOURCE, *glob.glob(os.path.join(INCLUDE, "*.h"))]):
+    if not force and bind_up_to_date():
         return BIND
     import torch
     where = os.path.dirname(torch.__file__)
@@ -73,11 +94,25 @@ def build_bind(force: bool = False) -> str:
         sys.stderr.write(res.stdout + res.stderr)
         raise RuntimeError("building _serving_bind.so failed")
     os.replace(tmp, BIND)
+    with open(tmp, "w") as f:
+        f.write(_bind_stamp())
+    os.replace(tmp, BIND_STAMP)
     return BIND
 
 
 def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = True) -> str:
-    build_bind(force)
+    """The library, and the extension where it can be built."""
+    build_library(force, ptxas_verbose, quiet)
+    try:
+        build_bind(force)
+    except (RuntimeError, ImportError, OSError) as e:
+        if os.path.exists(BIND) and not _bind_of_these_sources():
+            os.remove(BIND)  # it would call this library by another's signatures
+        sys.stderr.write(f"{LIB} is built; the serving calls' extension is not: {e}\n")
+    return LIB
+
+
+def build_library(force: bool = False, ptxas_verbose: bool = False, quiet: bool = True) -> str:
     if not force and up_to_date():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"

@@ -36,10 +36,10 @@ def _load_bind():
         from . import _serving_bind
     except ImportError as e:
         raise RuntimeError("the serving extension is not built for this Python and torch "
-                           "(run `python -m rank_biased_window_b200.build --force`)") from e
+                           "(run `python -m rank_biased_window_b200.build`)") from e
     if _serving_bind.torch_version != torch.__version__:
         raise RuntimeError(f"the serving extension was built for torch {_serving_bind.torch_version} "
-                           "(run `python -m rank_biased_window_b200.build --force`)")
+                           "(run `python -m rank_biased_window_b200.build`)")
     names = ("rfb_rotary", "rfb_cache_append", "rfb_attn_fwd_cache_workspace_size",
              "rfb_attn_fwd_cache_counts", "rfb_cache_evict", "rfb_strerror", "rfb_last_cuda_error")
     _serving_bind.init(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names))

@@ -181,3 +181,43 @@ def test_written_memory_is_apart(rfb_lib):
     for call, match in calls:
         with pytest.raises(ValueError, match=match.replace(" .* ", " must not share memory with ")):
             call()
+
+
+@pytest.fixture
+def elsewhere(rfb_lib, tmp_path, monkeypatch):
+    """The build module with its products in a folder of their own."""
+    import shutil
+    from rank_biased_window_b200 import build
+    for name in ("LIB", "BIND", "BIND_STAMP"):
+        here = tmp_path / os.path.basename(getattr(build, name))
+        shutil.copy2(getattr(build, name), here)
+        monkeypatch.setattr(build, name, str(here))
+    return build
+
+
+def test_library_is_built_without_the_extension(elsewhere, monkeypatch, capsys):
+    """Without a host compiler for the extension the library is built as ever, and no
+    extension of other sources is left beside it."""
+    made = []
+    monkeypatch.setattr(elsewhere, "build_library", lambda *a: made.append(os.path.exists(elsewhere.BIND)))
+    for cxx in ("/nonexistent/c++", "false"):
+        monkeypatch.setenv("CXX", cxx)
+        assert elsewhere.build(force=True) == elsewhere.LIB
+        assert "is not" in capsys.readouterr().err and os.path.exists(elsewhere.BIND)
+        with pytest.raises((RuntimeError, OSError)):
+            elsewhere.build_bind(force=True)
+    os.utime(elsewhere.BIND, (0, 0))
+    assert elsewhere.build() == elsewhere.LIB
+    assert "is not" in capsys.readouterr().err and not os.path.exists(elsewhere.BIND)
+    assert made == [True] * 3       # the library came first
+
+
+def test_extension_of_another_torch_is_built_again(elsewhere, monkeypatch):
+    assert elsewhere.bind_up_to_date()
+    monkeypatch.setenv("CXX", "false")
+    assert elsewhere.build_bind() == elsewhere.BIND            # nothing to do
+    monkeypatch.setattr(torch, "__version__", "1.0")
+    assert not elsewhere.bind_up_to_date()
+    with pytest.raises(RuntimeError, match="failed"):
+        elsewhere.build_bind()
+    monkeypatch.undo()
