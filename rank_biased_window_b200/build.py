@@ -58,7 +58,7 @@ def up_to_date() -> bool:
 
 
 def _bind_of_these_sources() -> bool:
-    return _newer(BIND, [BIND_SOURCE, *glob.glob(os.path.join(INCLUDE, "*.h"))])
+    return _newer(BIND, [BIND_SOURCE, os.path.abspath(__file__), *glob.glob(os.path.join(INCLUDE, "*.h"))])
 
 
 def _bind_stamp() -> str:
@@ -81,13 +81,19 @@ def build_bind(force: bool = False) -> str:
     where = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     tmp = BIND + f".tmp{os.getpid()}"
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC",
+    cxx = os.environ.get("CXX", "g++")
+    # torch's C++ runtime, by name: a compiler that finds no libstdc++.so links its archive
+    # instead, without a word, and a second runtime in the process crashes where its streams
+    # meet the first one's locales (a number put into one) and in exceptions across the two.
+    runtime = subprocess.run([cxx, "-print-file-name=libstdc++.so.6"], capture_output=True,
+                             text=True).stdout.strip()
+    cmd = [cxx, "-O2", "-std=c++17", "-shared", "-fPIC",
            "-fvisibility=hidden", f'-DRFB_TORCH_VERSION="{torch.__version__}"',
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE,
            "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(where, "include"),
            "-isystem", os.path.join(where, "include", "torch", "csrc", "api", "include"),
            "-isystem", os.path.join(cuda, "include"), "-L", os.path.join(where, "lib"),
-           "-o", tmp, BIND_SOURCE,
+           "-o", tmp, BIND_SOURCE, *([runtime] if os.path.isabs(runtime) else []),
            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:

@@ -16,6 +16,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
+#include <sstream>
 #include <string>
 
 #include "rfb_attn.h"
@@ -37,14 +38,11 @@ struct Refusal {
   PyObject* type;
   std::string text;
 };
-// Joined without streams: a number put into a std::ostringstream crashed in this
-// module (under the interpreter it was first tested with), text alone did not.
-std::string text(const char* s) { return s; }
-std::string text(const std::string& s) { return s; }
-std::string text(int64_t n) { return std::to_string(n); }
 template <typename... A>
 [[noreturn]] void refuse(PyObject* type, const A&... a) {
-  throw Refusal{type, (text(a) + ...)};
+  std::ostringstream s;
+  (s << ... << a);
+  throw Refusal{type, s.str()};
 }
 
 std::string shape_text(at::IntArrayRef s) {

@@ -221,3 +221,40 @@ def test_extension_of_another_torch_is_built_again(elsewhere, monkeypatch):
     with pytest.raises(RuntimeError, match="failed"):
         elsewhere.build_bind()
     monkeypatch.undo()
+
+
+def test_extension_shares_the_process_runtime(rfb_lib):
+    """One C++ runtime in the process: the extension takes torch's, so that numbers go
+    through its streams and torch's exceptions through its handlers (in a child, which a
+    second runtime ends by a signal)."""
+    import subprocess
+    import sys
+    code = """
+import torch
+from rank_biased_window_b200 import serving
+bind = serving._load_bind()
+c = torch.zeros(2, 2, 64, 64, dtype=torch.uint8).view(torch.float8_e4m3fn)
+s, n = torch.ones(2, 2, 2), torch.zeros(2, dtype=torch.int32)
+held = bind.cache(c, c.clone(), None, s, s.clone(), None)
+for H in (3, -1):
+    q = torch.zeros(2, abs(H), 1, 64, dtype=torch.bfloat16)
+    try:
+        if H > 0:
+            bind.attn(held, q, None, n, None, True, None, None, 1.0, None, None, None)
+        else:
+            bind.append(held, None, q, q[:0], None, n, None)
+    except ValueError as e:
+        print(e)
+try:                                     # an exception of torch's own, from one of its functions
+    q = torch.zeros(2, 2, 1, 64, dtype=torch.bfloat16)
+    bind.attn(held, q, None, n, None, True, None, None, 1.0, None, None, None)
+except RuntimeError as e:
+    print("torch:", len(str(e)) > 0)
+libs = {line.split()[-1] for line in open("/proc/self/maps") if "libstdc++" in line}
+print(len(libs))
+"""
+    p = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT)
+    assert p.returncode == 0, (p.returncode, p.stderr[-2000:])
+    assert p.stdout.splitlines() == ["3 query heads are not a multiple of the cache's 2",
+                                     "k has shape (2, 1, 1, 64), expected (2, 2, 1, 64)",
+                                     "torch: True", "1"]
