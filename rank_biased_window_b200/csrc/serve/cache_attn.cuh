@@ -9,13 +9,14 @@
 // (the order of channels and of tokens inside a contraction is free, so each
 // lane loads whole 8- or 16-byte pieces of rows and the queries are permuted to
 // match), become fp16 there (exact) and enter m16n8k16 MMAs with fp32
-// accumulators.  Softmax statistics and sums are fp32; the probabilities are
-// rounded to fp16 for the product with V (2^-11 relative, below the bf16
-// rounding of O), lifted by 2^11 so that this holds down to 2^-25 of the largest:
-// a token of small weight may have a large value.  The largest is followed with a
-// slack of 2^4, so that the sums are rescaled a few times a segment (2^15 is within
-// fp16).  Queries enter as fp16 scaled by a power of two per row, which holds every
-// bf16 within 2^-29 of the row's largest exactly.
+// accumulators.  Softmax statistics and sums are fp32; the probabilities enter the
+// product with V as two fp16 terms (2^-22 relative, so that O is what fp32 weights give:
+// with one, 2^-11, one value of O in thirty came out a bf16 step away; one is as fast
+// where the bytes bind and takes 33.3 us for 34.9 at 64 rows), lifted by 2^11 so that the
+// first is normal down to 2^-25 of the largest: a token of small weight may have a large
+// value.  The largest is followed with a slack of 2^4, so that the sums are rescaled a few
+// times a segment (2^15 is within fp16).  Queries enter as fp16 scaled by a power of two
+// per row, which holds every bf16 within 2^-28 of the row's largest exactly.
 //
 // Bound by HBM for few rows: 2 d + r bytes a token and head (2 x 131000 tokens of
 // 8 heads, d = 64, r = 32: 60.5 us, 5.6 TB/s; 16 sequences of up to 8190 tokens, 32
@@ -198,11 +199,12 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   return r;
 }
 
-// O^T += V^T P^T for 16 tokens and 8 QT queries: v[i] the lane's piece of its i-th
+// O^T += V^T P^T for 16 tokens and 8 QT queries, P in two fp16 terms (p[q][0..1] and the
+// rest of the fp32 weight, p[q][2..3]): v[i] the lane's piece of its i-th
 // token (two of columns 2 t, 2 t + 1, two of the next 8), word w of it, i.e. channels
 // g (D / 8) + 4 w + {0..3}, which are rows g and g + 8 of channel tiles 2 w, 2 w + 1.
 template <int VW, int QT>
-__device__ __forceinline__ void pv_words(const uint32_t (*p)[2], const uint32_t (*v)[VW], int w,
+__device__ __forceinline__ void pv_words(const uint32_t (*p)[4], const uint32_t (*v)[VW], int w,
                                          float (*o)[QT][4]) {
   const uint32_t a01 = __byte_perm(v[0][w], v[1][w], 0x5140);
   const uint32_t a23 = __byte_perm(v[0][w], v[1][w], 0x7362);
@@ -214,10 +216,12 @@ __device__ __forceinline__ void pv_words(const uint32_t (*p)[2], const uint32_t 
   for (int q = 0; q < QT; ++q) {
     mma_f16(o[0][q], lo, p[q][0], p[q][1]);
     mma_f16(o[1][q], hi, p[q][0], p[q][1]);
+    mma_f16(o[0][q], lo, p[q][2], p[q][3]);
+    mma_f16(o[1][q], hi, p[q][2], p[q][3]);
   }
 }
 template <int VW, int QT>
-__device__ __forceinline__ void pv_step(const uint32_t (*p)[2], const uint32_t (*v)[VW],
+__device__ __forceinline__ void pv_step(const uint32_t (*p)[4], const uint32_t (*v)[VW],
                                         float (*o)[QT][4]) {
 #pragma unroll
   for (int w = 0; w < VW; ++w) pv_words<VW, QT>(p, v, w, o + 2 * w);
@@ -335,7 +339,7 @@ __device__ __forceinline__ void load_v(uint32_t (*v)[D / 32], uint32_t vrow, int
 // token that only some queries see would reach the others through 0 x NaN: such a
 // block goes query by query, with the tokens that it does not see as zeros.
 template <int D, int QT>
-__device__ __noinline__ void pv_edge_queries(const uint32_t (*p)[QT][2], uint32_t vrow, int tok0,
+__device__ __noinline__ void pv_edge_queries(const uint32_t (*p)[QT][4], uint32_t vrow, int tok0,
                                              const int (*lim)[2], float (*o)[QT][4]) {
   constexpr int VW = D / 32;
   const int lane = lane_id(), g = lane >> 2, t = lane & 3;
@@ -346,10 +350,10 @@ __device__ __noinline__ void pv_edge_queries(const uint32_t (*p)[QT][2], uint32_
       const int lim_r = __shfl_sync(0xffffffffu, r & 1 ? lim[q][1] : lim[q][0], r >> 1);
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) {
-        uint32_t pr[1][2], v[4][VW];
+        uint32_t pr[1][4], v[4][VW];
         load_v<D>(v, vrow, kk, t);
-        pr[0][0] = g == r ? p[kk][q][0] : 0u;
-        pr[0][1] = g == r ? p[kk][q][1] : 0u;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) pr[0][k] = g == r ? p[kk][q][k] : 0u;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           if (tok0 + piece_token(kk, k, t) >= lim_r)
@@ -372,7 +376,7 @@ __device__ __noinline__ void pv_edge_queries(const uint32_t (*p)[QT][2], uint32_
     }
 }
 template <int D, int QT>
-__device__ __forceinline__ void pv_edge(const uint32_t (*p)[QT][2], uint32_t vrow, int tok0, int L,
+__device__ __forceinline__ void pv_edge(const uint32_t (*p)[QT][4], uint32_t vrow, int tok0, int L,
                                         const int (*lim)[2], bool masked, float (*o)[QT][4]) {
   constexpr int VW = D / 32;
   const int t = lane_id() & 3;
@@ -389,15 +393,14 @@ __device__ __forceinline__ void pv_edge(const uint32_t (*p)[QT][2], uint32_t vro
   }
   if (masked && __any_sync(0xffffffffu, nan != 0)) {
     float c[D / 16][QT][4] = {};
-    uint32_t pc[2][QT][2];
+    uint32_t pc[2][QT][4];
     int lc[QT][2];
 #pragma unroll
-    for (int q = 0; q < QT; ++q)
+    for (int q = 0; q < QT; ++q) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        pc[0][q][k] = p[0][q][k], pc[1][q][k] = p[1][q][k];
-        lc[q][k] = lim[q][k];
-      }
+      for (int k = 0; k < 4; ++k) pc[0][q][k] = p[0][q][k], pc[1][q][k] = p[1][q][k];
+      lc[q][0] = lim[q][0], lc[q][1] = lim[q][1];
+    }
     pv_edge_queries<D, QT>(pc, vrow, tok0, lc, c);
 #pragma unroll
     for (int n = 0; n < D / 16; ++n)
@@ -737,7 +740,7 @@ __global__ void __launch_bounds__(kCaThreads, 3)
             for (int k = 0; k < 4; ++k) oacc[n][q][k] *= al[k & 1];
         }
       }
-      uint32_t p[2][QT][2];
+      uint32_t p[2][QT][4];
 #pragma unroll
       for (int q = 0; q < QT; ++q) {
 #pragma unroll
@@ -747,8 +750,14 @@ __global__ void __launch_bounds__(kCaThreads, 3)
             x[j][q][k] = fast_exp2(x[j][q][k] - m[q][k & 1]);
             l[q][k & 1] += x[j][q][k];
           }
-          p[j][q][0] = transpose8x8(pack_f16x2(x[j][q][0], x[j][q][1]));
-          p[j][q][1] = transpose8x8(pack_f16x2(x[j][q][2], x[j][q][3]));
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t high = pack_f16x2(x[j][q][2 * e], x[j][q][2 * e + 1]);
+            const float2 h = f16x2_to_f32x2(high);
+            p[j][q][e] = transpose8x8(high);
+            p[j][q][2 + e] =
+                transpose8x8(pack_f16x2(x[j][q][2 * e] - h.x, x[j][q][2 * e + 1] - h.y));
+          }
         }
       }
       // O^T += V^T P^T

@@ -251,3 +251,35 @@ def test_counts_are_read_on_the_device_and_checked(rfb_lib, cuda_dev):
         eo, el = rfb_lib.attn_fwd_cache(q, None, cache, L, counts=c)
         assert torch.equal(o, eo) and torch.equal(lse, el)
         assert bool((lse[0, :, v[0]:] == float("-inf")).all()) and bool((lse[0, :, : v[0]] > -1e9).all())
+
+
+@pytest.mark.parametrize("d,r,Nq,cap,L", [
+    (64, 0, 1, 512, 512), (64, 8, 1, 4096, 4001), (128, 0, 1, 512, 77), (32, 16, 9, 512, 300),
+    (64, 16, 9, 4096, 4096), (128, 64, 40, 512, 500), (64, 0, 70, 4096, 3999)])
+def test_attention_weights_keep_fp32(rfb_lib, cuda_dev, d, r, Nq, cap, L):
+    """Nearly equal weights on values that cancel: what is left shows each weight's rounding.
+
+    A weight is off by its exponent's rounding (|x - m| < 16: 2^-21), the exponential's 2^-22
+    and its two fp16 terms' 2^-22, a product by its sum's 2^-22; together below 2^-19 of
+    sum p |v|, where one fp16 term would be off by 2^-12 a weight.  The common factor of a
+    row and bf16 are relative to O."""
+    g = gen(d + cap)
+    cache = rfb_lib.Cache8.create(1, 1, cap, d, r, device=cuda_dev)
+    k, v = torch.randn(cap, d, generator=g) * 64, torch.randn(cap // 2, d, generator=g) * 64
+    cache.k.copy_(k.to(ref.E4M3)[None, None])
+    cache.v.copy_(torch.stack((v, -v), 1).view(cap, d).to(ref.E4M3)[None, None])
+    if r:
+        cache.w.copy_((torch.randn(cap, r, generator=g) * 64).to(ref.E4M3)[None, None])
+    val = {m: cache.values(m).cpu().double() for m in ("k", "v") + (("w",) if r else ())}
+    q = (torch.randn(1, 2, Nq, d, generator=g) * 2.0 ** -20).bfloat16()
+    u = (torch.randn(1, 2, Nq, r, generator=g) * 2.0 ** -20).bfloat16() if r else None
+    o, _ = rfb_lib.attn_fwd_cache(q.to(cuda_dev), u.to(cuda_dev) if r else None, cache, ints([L], cuda_dev),
+                                  1.0, causal=False)
+    x = q.double() @ val["k"][0, 0, :L].T
+    if r:
+        x = x + u.double() @ val["w"][0, 0, :L].T
+    assert float(x.abs().max()) < 2.0 ** -5     # so a score's own rounding is below 2^-23
+    p = torch.softmax(x, -1)
+    want = p @ val["v"][0, 0, :L]
+    room = 2.0 ** -19 * (p @ val["v"][0, 0, :L].abs()) + (2.0 ** -8 + 2.0 ** -16) * want.abs()
+    ref.assert_within("o", o, want, room)
