@@ -6,8 +6,9 @@
 // backward is the same kernel with -t on the gradients.
 //
 // The angle is formed in turns in fp64 and reduced there (fp32 would lose the
-// angle of far positions), the sine and cosine of the remainder in fp32; that
-// work is done once per token and pair and used for every head of q and k the
+// angle of far positions); sine and cosine of the remainder's fp32 value are turned by
+// what that leaves (up to 2^-26 of a turn, more than fp32's rounding of a sine near 0);
+// that work is done once per token and pair and used for every head of q and k the
 // thread goes over.  One read and one write of q and k: bound by HBM (2 x 16384 tokens,
 // 8 + 8 heads, d = 64, forward and backward: 47.5 us, 5.7 TB/s; 4097 tokens of 16 fp32
 // heads, d = 128: 10.6 us, 6.3 TB/s).
@@ -96,10 +97,13 @@ struct Rot<__half> {
 // a cos t, +-a sin t of t = pos f.
 __device__ __forceinline__ void rot_angle(const RotArgs& a, int pos, int pair, float& c, float& s) {
   const double turns = static_cast<double>(pos) * a.freq[pair] * 0.15915494309189535;  // 1 / 2 pi
-  const float r = static_cast<float>(turns - rint(turns));
-  sincospif(2.0f * r, &s, &c);
-  c *= a.amp;
-  s *= a.amp * a.sign;
+  const double part = turns - rint(turns);
+  const float r = static_cast<float>(part);
+  const float rest = static_cast<float>(part - r) * 6.2831853f;  // |rest| < 2^-23
+  float s0, c0;
+  sincospif(2.0f * r, &s0, &c0);
+  c = fmaf(-s0, rest, c0) * a.amp;
+  s = fmaf(c0, rest, s0) * (a.amp * a.sign);
 }
 
 // VEC_OK: 16-byte vectors.  A unit is, in the half layout, VEC pairs (one

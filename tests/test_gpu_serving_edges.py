@@ -283,3 +283,27 @@ def test_attention_weights_keep_fp32(rfb_lib, cuda_dev, d, r, Nq, cap, L):
     want = p @ val["v"][0, 0, :L]
     room = 2.0 ** -19 * (p @ val["v"][0, 0, :L].abs()) + (2.0 ** -8 + 2.0 ** -16) * want.abs()
     ref.assert_within("o", o, want, room)
+
+
+@pytest.mark.parametrize("inverse", [False, True])
+@pytest.mark.parametrize("amplitude", [1.0, 1.25])
+def test_rotary_angles_near_half_turns(rfb_lib, cuda_dev, inverse, amplitude):
+    """Angles 2^-5 to 2^-16 off a half or whole turn: the sine is as small as that, and
+    right to fp32's own steps, not to those of an angle of half a turn.
+
+    Room: the sine's ulp and half, the rounding of the product with the amplitude and of
+    the rotation (2^-24 each) make 2^-22 of the value; the angle in 64 bits is 2^-52 of
+    itself off here and in the definition."""
+    turns = torch.tensor([k / 2 + sign * (2.0 ** -e + j * 2.0 ** -29.7)
+                          for k in (0, 1, 7, 101) for sign in (-1, 1) for e in (5, 9, 13, 16)
+                          for j in range(8)], dtype=torch.float64)
+    freqs = (turns * 2 * torch.pi / 7.0).abs()      # at position 7
+    rot = 2 * freqs.numel()
+    x = torch.zeros(1, 1, 2, rot)
+    x[..., : rot // 2] = 1.0
+    pos = torch.tensor([7, -7], dtype=torch.int32)
+    turn = rfb_lib.rotary_bwd if inverse else rfb_lib.rotary_fwd
+    y, _ = turn(x.to(cuda_dev), None, pos.to(cuda_dev), freqs.to(cuda_dev), amplitude=amplitude)
+    want, _ = ref.rotary(x, pos, freqs, "half", amplitude, inverse=inverse)
+    angle = pos.double()[None, None, :, None] * torch.cat((freqs, freqs))
+    ref.assert_within("y", y, want, want.abs() * 2.0 ** -22 + angle.abs() * amplitude * 2.0 ** -51)
