@@ -334,6 +334,8 @@ RFB_API int rfb_rotary(const void* q, const void* k, void* q_out, void* k_out,
  * cap is a multiple of 32 (the capacity in tokens); sequence lengths are device
  * int32 arrays [B], read when the kernels run, and clamped to [0, cap].  What
  * lies behind a sequence's length is neither read into a result nor changed.
+ * Codes, rows, queries, factors and O are 16-byte aligned; scales, masses, LSE and integers as
+ * their elements are, so that views of single sequences or heads are caches too.
  *
  * Append: rows start[b] .. start[b] + counts[b] - 1 of the cache receive the
  * first counts[b] of the n new rows; rows that would fall at or behind cap are

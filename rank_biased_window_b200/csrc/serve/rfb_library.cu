@@ -294,14 +294,14 @@ int rfb_cache_append(const void* k, const void* v, const void* w, const long lon
   float* s[3] = {k_scale, v_scale, w_scale};
   a.tensors = r > 0 ? 3 : 2;
   for (int z = 0; z < a.tensors; ++z) {
-    if (!aligned16(x[z]) || !aligned16(c[z]) || !aligned16(s[z])) return RFB_ERR_ALIGNMENT;
+    if (!aligned16(x[z]) || !aligned16(c[z]) || !aligned_to(s[z], 4)) return RFB_ERR_ALIGNMENT;
     a.x[z] = static_cast<const __nv_bfloat16*>(x[z]);
     a.codes[z] = static_cast<uint8_t*>(c[z]);
     a.scales[z] = s[z];
     a.sb[z] = strides[3 * z], a.sh[z] = strides[3 * z + 1], a.sn[z] = strides[3 * z + 2];
     if (a.sb[z] % 8 || a.sh[z] % 8 || a.sn[z] % 8) return RFB_ERR_ALIGNMENT;
   }
-  if (!aligned16(mass) || !aligned_to(start, 4) || !aligned_to(counts, 4)) return RFB_ERR_ALIGNMENT;
+  if (!aligned_to(mass, 4) || !aligned_to(start, 4) || !aligned_to(counts, 4)) return RFB_ERR_ALIGNMENT;
   a.mass = mass;
   a.start = start;
   a.counts = counts;
@@ -361,7 +361,8 @@ int rfb_attn_fwd_cache_counts(const void* q, const void* u, const void* k8, cons
   if (R == 0) {
     if (cap > 65535 * 128) return RFB_ERR_UNSUPPORTED;
     if (!lengths) return RFB_ERR_INVALID_ARG;
-    if (!aligned16(mass) || !aligned16(mass_out) || !aligned_to(lengths, 4)) return RFB_ERR_ALIGNMENT;
+    if (!aligned_to(mass, 4) || !aligned_to(mass_out, 4) || !aligned_to(lengths, 4))
+      return RFB_ERR_ALIGNMENT;
     CacheAttnArgs a = {};
     a.lengths = lengths;
     a.mass = mass, a.mass_out = mass_out, a.decay = decay;
@@ -377,9 +378,9 @@ int rfb_attn_fwd_cache_counts(const void* q, const void* u, const void* k8, cons
       (cap > 0 && (!k8 || !v8 || !k_scale || !v_scale || (r > 0 && (!w8 || !w_scale)))))
     return RFB_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(u) || !aligned16(k8) || !aligned16(v8) || !aligned16(w8) ||
-      !aligned16(o) || !aligned16(lse) || !aligned16(k_scale) || !aligned16(v_scale) ||
-      !aligned16(w_scale) || !aligned16(mass) || !aligned16(mass_out) || !aligned_to(lengths, 4) ||
-      !aligned_to(counts, 4))
+      !aligned16(o) || !aligned_to(lse, 4) || !aligned_to(k_scale, 4) || !aligned_to(v_scale, 4) ||
+      !aligned_to(w_scale, 4) || !aligned_to(mass, 4) || !aligned_to(mass_out, 4) ||
+      !aligned_to(lengths, 4) || !aligned_to(counts, 4))
     return RFB_ERR_ALIGNMENT;
   DeviceInfo dev;
   if (int rc = current_device(&dev)) return rc;
@@ -439,7 +440,7 @@ int rfb_cache_evict(const void* k8, const void* v8, const void* w8, const float*
   int same = 0;
   for (int z = 0; z < a.tensors; ++z) {
     if (!c[z] || !co[z] || !s[z] || !so[z]) return RFB_ERR_INVALID_ARG;
-    if (!aligned16(c[z]) || !aligned16(co[z]) || !aligned16(s[z]) || !aligned16(so[z]))
+    if (!aligned16(c[z]) || !aligned16(co[z]) || !aligned_to(s[z], 4) || !aligned_to(so[z], 4))
       return RFB_ERR_ALIGNMENT;
     same += (c[z] == co[z]) + (s[z] == so[z]);
     a.codes[z] = static_cast<const uint8_t*>(c[z]);
@@ -449,7 +450,7 @@ int rfb_cache_evict(const void* k8, const void* v8, const void* w8, const float*
   }
   if (!mass || !mass_out || !lengths || !new_lengths || !kept || lengths == new_lengths)
     return RFB_ERR_INVALID_ARG;
-  if (!aligned16(mass) || !aligned16(mass_out) || !aligned_to(lengths, 4) ||
+  if (!aligned_to(mass, 4) || !aligned_to(mass_out, 4) || !aligned_to(lengths, 4) ||
       !aligned_to(new_lengths, 4) || !aligned_to(kept, 4))
     return RFB_ERR_ALIGNMENT;
   same += mass == mass_out;

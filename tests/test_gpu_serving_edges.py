@@ -307,3 +307,36 @@ def test_rotary_angles_near_half_turns(rfb_lib, cuda_dev, inverse, amplitude):
     want, _ = ref.rotary(x, pos, freqs, "half", amplitude, inverse=inverse)
     angle = pos.double()[None, None, :, None] * torch.cat((freqs, freqs))
     ref.assert_within("y", y, want, want.abs() * 2.0 ** -22 + angle.abs() * amplitude * 2.0 ** -51)
+
+
+def test_views_of_single_sequences(rfb_lib, cuda_dev):
+    """A cache and outputs that are views of one sequence each, whose scales, LSE and
+    lengths lie at any 4-byte boundary, as the whole batch's calls."""
+    B, H, Nq, cap, d, r = 3, 3, 1, 96, 64, 8
+    names = ("k", "v", "w", "k_scale", "v_scale", "w_scale", "mass")
+    whole, _ = filled(rfb_lib, cuda_dev, B, 1, cap, d, r, seed=7, mass=True)
+    parts, _ = filled(rfb_lib, cuda_dev, B, 1, cap, d, r, seed=7, mass=True)
+    g = gen(9)
+    x = [torch.randn(B, 1, 2, c, generator=g).bfloat16().to(cuda_dev) for c in (d, d, r)]
+    q, u = (torch.randn(B, H, Nq, c, generator=g).bfloat16().to(cuda_dev) for c in (d, r))
+    start, lengths = ints([30, 63, 80], cuda_dev), ints([32, 65, 82], cuda_dev)
+    rfb_lib.cache_append(whole, *x, start=start)
+    o, lse = rfb_lib.attn_fwd_cache(q, u, whole, lengths, mass=whole.mass, mass_out=whole.mass)
+    new, kept = rfb_lib.cache_evict(whole, lengths, 40, 5)
+    got_lse = torch.zeros(B, H, Nq, device=cuda_dev)
+    for b in range(B):
+        s = slice(b, b + 1)
+        one = rfb_lib.Cache8(*(getattr(parts, n)[s] for n in names))
+        assert b == 0 or one.k_scale.data_ptr() % 16 and got_lse[s].data_ptr() % 16
+        rfb_lib.cache_append(one, *(t[s] for t in x), start=start[s])
+        ob, lb = rfb_lib.attn_fwd_cache(q[s], u[s], one, lengths[s], mass=one.mass, mass_out=one.mass,
+                                        lse=got_lse[s])
+        nb, kb = rfb_lib.cache_evict(one, lengths[s], 40, 5)
+        assert torch.equal(ob, o[s]) and torch.equal(lb, lse[s])
+        assert torch.equal(nb, new[s]) and torch.equal(kb, kept[s])
+        empty = torch.empty(1, 3, 0, d, dtype=torch.bfloat16, device=cuda_dev)
+        rfb_lib.attn_fwd_cache(empty, u[s, :, :0], one, lengths[s], mass=one.mass, mass_out=one.mass)
+    for n in names:
+        a, b = (getattr(c, n).view(torch.uint8) for c in (whole, parts))
+        assert torch.equal(a, b), n
+    assert torch.equal(got_lse, lse)
