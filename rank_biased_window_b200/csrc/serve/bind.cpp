@@ -93,8 +93,9 @@ void apart(const char* name, const at::Tensor& x, const char* other, const at::T
 }
 // The memory of a contiguous tensor.
 struct Span {
-  const char* name;
-  const char *lo, *hi;
+  const char* name = "";
+  const char *lo = nullptr, *hi = nullptr;
+  Span() = default;
   Span(const char* n, const at::Tensor& t)
       : name(n), lo(t.defined() ? static_cast<const char*>(t.const_data_ptr()) : nullptr),
         hi(t.defined() ? lo + t.numel() * t.element_size() : nullptr) {}
@@ -253,23 +254,22 @@ struct Cache {
   at::Tensor t[6];  // k, v, w, their scales; w and its scale may be undefined
   int64_t B, Hk, cap, d, r;
   at::Device on{at::kCPU};
-  Span span(int i) const { return Span(kPart[i], t[i]); }
+  Span span[6];        // where they lay when the cache was made
+  bool meets = false;  // one in another's memory
   // For the calls that write the tensors: none may lie in another's memory or in the mass's.
   void own_memory(const Span& mass) const {
-    const Span all[7] = {span(0), span(1), span(2), span(3), span(4), span(5), mass};
-    for (int i = 0; i < 7; ++i)
-      for (int k = 0; k < i; ++k) all[i].apart(all[k]);
+    for (int i = 0; meets && i < 6; ++i)
+      for (int k = 0; k < i; ++k) span[i].apart(span[k]);
+    for (const Span& x : span) mass.apart(x);
   }
   // What a tensor was at the start it may no longer be (resize_, set_, .data, a freed storage).
   bool as_made(int i) const {
     const at::Tensor& x = t[i];
     if (!x.defined()) return true;
     const int64_t c = i < 2 ? d : r;
-    return (i < 3 ? x.sizes() == at::IntArrayRef({B, Hk, cap, c})
-                  : x.sizes() == at::IntArrayRef({B, Hk, cap / 32})) &&
-           x.is_contiguous() && x.device() == on &&
-           x.scalar_type() == (i < 3 ? at::kFloat8_e4m3fn : at::kFloat) &&
-           x.storage().nbytes() >= (x.storage_offset() + x.numel()) * x.element_size();
+    return x.const_data_ptr() == span[i].lo && x.is_contiguous() &&
+           (i < 3 ? x.sizes() == at::IntArrayRef({B, Hk, cap, c})
+                  : x.sizes() == at::IntArrayRef({B, Hk, cap / 32}));
   }
   void* ptr(int i) const { return t[i].defined() ? t[i].data_ptr() : nullptr; }
   float* scale(int i) const { return static_cast<float*>(ptr(3 + i)); }
@@ -284,7 +284,7 @@ Cache& cache_of(PyObject* o) {
   for (int i = 0; i < 6; ++i)
     if (!c.as_made(i))
       refuse(PyExc_ValueError, kPart[i],
-             " is not what it was when the cache was made (size, layout, type, device or storage)");
+             " is not what it was when the cache was made (size, layout or memory)");
   return c;
 }
 
@@ -296,6 +296,10 @@ PyObject* cache(PyObject* const* a) {
   c->B = c->t[0].size(0), c->Hk = c->t[0].size(1), c->cap = c->t[0].size(2), c->d = c->t[0].size(3);
   c->r = c->t[2].defined() ? c->t[2].size(3) : 0;
   c->on = c->t[0].device();
+  for (int i = 0; i < 6; ++i) {
+    c->span[i] = Span(kPart[i], c->t[i]);
+    for (int k = 0; k < i; ++k) c->meets |= c->span[i].meets(c->span[k]);
+  }
   return PyCapsule_New(c, kCacheName, [](PyObject* o) {
     delete static_cast<Cache*>(PyCapsule_GetPointer(o, kCacheName));
   });
@@ -409,18 +413,20 @@ PyObject* attn(PyObject* const* a) {
       refuse(PyExc_ValueError, "workspace must be a contiguous tensor on ", device_text(dev));
   }
   // what is written, of the caller's: apart from what is read and from one another
-  const auto given = [&](int i) { return a[i] == Py_None ? at::Tensor() : THPVariable_Unpack(a[i]); };
-  const Span written[4] = {{"out", out}, {"lse", lse}, {"workspace", ws}, {"mass_out", given(7)}};
-  const Span read[4] = {{"q", q}, {"u", given(2)}, {"lengths", lengths}, {"counts", given(12)}};
-  const Span mass_in("mass", given(6));
-  for (int i = 0; i < 4; ++i) {
-    const Span& x = written[i];
-    if (x.lo == x.hi) continue;
-    for (int k = 0; k < i; ++k) x.apart(written[k]);
-    for (const Span& y : read) x.apart(y);
-    for (int k = 0; k < 6; ++k) x.apart(c.span(k));
-    if (i < 3) x.apart(mass_in);
-    else x.same_or_apart(mass_in);
+  if (out.defined() || lse.defined() || ws.defined() || mass_out) {
+    const auto given = [&](int i) { return a[i] == Py_None ? at::Tensor() : THPVariable_Unpack(a[i]); };
+    const Span written[4] = {{"out", out}, {"lse", lse}, {"workspace", ws}, {"mass_out", given(7)}};
+    const Span read[4] = {{"q", q}, {"u", given(2)}, {"lengths", lengths}, {"counts", given(12)}};
+    const Span mass_in("mass", given(6));
+    for (int i = 0; i < 4; ++i) {
+      const Span& x = written[i];
+      if (x.lo == x.hi) continue;
+      for (int k = 0; k < i; ++k) x.apart(written[k]);
+      for (const Span& y : read) x.apart(y);
+      for (const Span& y : c.span) x.apart(y);
+      if (i < 3) x.apart(mass_in);
+      else x.same_or_apart(mass_in);
+    }
   }
   Launch on(dev);
   if (!out.defined()) out = make(q.sizes(), at::kBFloat16, dev);
@@ -448,12 +454,13 @@ PyObject* evict(PyObject* const* a) {
   // each tensor in the place of its own kind or in no other's
   to.own_memory(Span("the cache's mass", to_mass));
   if (&c != &to) {
-    Span from[7] = {c.span(0), c.span(1), c.span(2), c.span(3), c.span(4), c.span(5), {"", mass}};
-    Span into[7] = {to.span(0), to.span(1), to.span(2), to.span(3), to.span(4), to.span(5), {"", to_mass}};
-    for (int i = 0; i < 7; ++i) {
-      into[i].name = "out", from[i].name = "the cache";
-      for (int k = 0; k < 7; ++k) i == k ? into[i].same_or_apart(from[k]) : into[i].apart(from[k]);
-    }
+    const Span from("", mass), into("", to_mass);
+    for (int i = 0; i < 7; ++i)
+      for (int k = 0; k < 7; ++k) {
+        const Span &x = i < 6 ? to.span[i] : into, &y = k < 6 ? c.span[k] : from;
+        if (x.meets(y) && !(i == k && x.lo == y.lo))
+          refuse(PyExc_ValueError, "out must not share memory with the cache");
+      }
   }
   const int keep = small(integer(a[5]), "keep"), recent = small(integer(a[6]), "recent");
   Launch on(dev);
