@@ -176,8 +176,12 @@ class RFBRotary(torch.autograd.Function):
 
         def rows(t):
             return t if t is None or t.stride(3) == 1 or t.shape[3] == 1 else t.contiguous()
-        gq, gk = RFBRotary.apply(rows(dq), rows(dk), positions, freqs, ctx.layout, ctx.amplitude,
-                                 not ctx.inverse)
+        # a gradient that nobody wants (a frozen q, or k) is not turned
+        need_q, need_k = ctx.needs_input_grad[:2]
+        first, second = (rows(dq), rows(dk) if need_k else None) if need_q else (rows(dk), None)
+        grads = RFBRotary.apply(first, second, positions, freqs, ctx.layout, ctx.amplitude,
+                                not ctx.inverse)
+        gq, gk = grads if need_q else (None, grads[0])
         return gq, gk, None, None, None, None, None
 
 

@@ -340,3 +340,29 @@ def test_views_of_single_sequences(rfb_lib, cuda_dev):
         a, b = (getattr(c, n).view(torch.uint8) for c in (whole, parts))
         assert torch.equal(a, b), n
     assert torch.equal(got_lse, lse)
+
+
+@pytest.mark.parametrize("need_q,need_k", [(True, True), (True, False), (False, True)])
+def test_rotary_backward_turns_what_is_wanted(rfb_lib, cuda_dev, monkeypatch, need_q, need_k):
+    """With q or k frozen the backward turns the other's gradient alone, to the same bits;
+    gradients of gradients go the same way."""
+    from rank_biased_window_b200 import serving
+    g = gen(17)
+    q, k, dq, dk = (torch.randn(2, h, 5, 32, generator=g).to(cuda_dev) for h in (4, 2, 4, 2))
+    f, _ = rfb_lib.rotary_frequencies(32, device=cuda_dev)
+    pos = ints(list(range(5)), cuda_dev)
+    want = rfb_lib.rotary_bwd(dq, dk, pos, f)
+    q.requires_grad_(need_q), k.requires_grad_(need_k)
+    dq.requires_grad_(), dk.requires_grad_()
+    qo, ko = rfb_lib.rfb_rotary(q, k, pos, f)
+    turned, turn = [], serving.rotary_bwd
+    monkeypatch.setattr(serving, "rotary_bwd", lambda a, b, *r, **kw: turned.append(
+        [t is not None and t.shape[1] for t in (a, b)]) or turn(a, b, *r, **kw))
+    inputs = [t for t, n in ((q, need_q), (k, need_k)) if n]
+    got = torch.autograd.grad([qo, ko], inputs, [dq, dk], create_graph=True)
+    assert turned == [[4, 2] if need_q and need_k else [4, False] if need_q else [2, False]]
+    for a, b in zip(got, [w for w, n in zip(want, (need_q, need_k)) if n]):
+        assert torch.equal(a, b)
+    z = torch.randn(got[0].shape, generator=g).to(cuda_dev)
+    back, = torch.autograd.grad(got[0], dq if need_q else dk, z)
+    assert torch.equal(back, rfb_lib.rotary_fwd(z, None, pos, f)[0])
