@@ -3,29 +3,33 @@
 //
 //     x_t = s ks (q . k8_t) + ws (u . w8_t),   O = sum_t exp(x_t - LSE) vs v8_t.
 //
-// The rows of one key head (its query heads times the new tokens) share every
-// cached byte.  A warp takes 16 rows and walks over blocks of 32 tokens: the
-// codes go from global memory straight into the registers that the MMA wants
-// (the order of channels and of tokens inside a contraction is free, so each
-// lane loads whole 8- or 16-byte pieces of rows and the queries are permuted to
-// match), become fp16 there (exact) and enter m16n8k16 MMAs with fp32
-// accumulators.  Softmax statistics and sums are fp32; the probabilities enter the
+// The rows of one key head (its query heads times the new tokens) share every cached
+// byte.  A warp takes 8 or 16 rows and walks over blocks of 32 tokens, which one lane a
+// tensor copies (bulk copies with mbarriers) into a ring in shared memory, as they lie
+// in global memory; up to four warps of other rows share a ring.  From there each lane
+// reads whole 8- or 16-byte pieces of rows (the order of channels and of tokens inside a
+// contraction is free, so the queries are permuted to match), which become fp16 in
+// registers (exact) and enter m16n8k16 MMAs with fp32 accumulators, keys and values as
+// the row operand.  Softmax statistics and sums are fp32; the probabilities enter the
 // product with V as two fp16 terms (2^-22 relative, so that O is what fp32 weights give:
-// with one, 2^-11, one value of O in thirty came out a bf16 step away; one is as fast
-// where the bytes bind and takes 33.3 us for 34.9 at 64 rows), lifted by 2^11 so that the
-// first is normal down to 2^-25 of the largest: a token of small weight may have a large
-// value.  The largest is followed with a slack of 2^4, so that the sums are rescaled a few
-// times a segment (2^15 is within fp16).  Queries enter as fp16 scaled by a power of two
-// per row, which holds every bf16 within 2^-28 of the row's largest exactly.
+// with one, 2^-11, one value of O in twelve came out a bf16 step away, with two one in a
+// thousand; one takes 33.3 us for 34.9 at 64 rows, 196 for 207 at 450 sequences to 4096
+// tokens, and is no faster where the bytes bind), lifted by 2^11 so that the first is
+// normal down to 2^-25 of the largest: a token of small weight may have a large value.
+// The largest is followed with a slack of 2^4, so that the sums are rescaled a few times
+// a segment (2^15 is within fp16).  Queries enter as fp16 scaled by a power of two per
+// row, which holds every bf16 within 2^-28 of the row's largest exactly.
 //
 // Bound by HBM for few rows: 2 d + r bytes a token and head (2 x 131000 tokens of
-// 8 heads, d = 64, r = 32: 60.5 us, 5.6 TB/s; 16 sequences of up to 8190 tokens, 32
-// heads on 8, d = 128: 34.5 us, 4.4 TB/s; about 10 us of each are the start and the end
-// of the two kernels); by issue and latency for the 64 rows of 16 queries (8 sequences
-// of up to 5003 tokens, 16 heads on 4: 30.5 us with the weights, 21.5 without).  With at
+// 8 heads, d = 64, r = 32: 60.6 us, 5.6 TB/s; 16 sequences of up to 8190 tokens, 32
+// heads on 8, d = 128: 35.6 us, 4.2 TB/s; some 7 to 10 us of each are the start and the
+// end of the two kernels); by issue and latency for the 64 rows of 16 queries (8 sequences
+// of up to 5003 tokens, 16 heads on 4: 34.9 us with the weights, 24.9 without).  With at
 // most 16 rows in a tile, 32 flop per byte, the register-level MMA runs at a fraction
-// of its rate; tcgen05 would need the codes widened into shared memory first, which
-// costs more than the product.
+// of its rate and the bytes bind.  tcgen05 could multiply the codes as they are
+// (kind::f8f6f4), but its other operand is 8 bits then too, with 4 of them significant:
+// a bf16 query would take two terms and a weight of 22 bits six, and of a tile's 128 rows
+// 64 at most are there.  Not measured.
 //
 // Work split: the blocks of all (sequence, key head, row tile) segments form one
 // line, cut into equal parts, one per CTA, so ragged lengths and few long
@@ -996,8 +1000,8 @@ __device__ __forceinline__ void store_mass(const CacheAttnArgs& a, long long at,
 
 // mass_out = decay mass + sum over the key head's rows of exp(x - LSE).  Up to 8
 // rows leave their scores in the workspace (8 bytes of traffic a row and token, less
-// than reading K again: a decode step 24.0 us against 37.1, 8 rows a key head 15.1
-// against 17.5); with more rows the scores are computed again, beside the join
+// than reading K again: a decode step 25.1 us against 39.5, 8 rows a key head 16.2
+// against 19.3); with more rows the scores are computed again, beside the join
 // where a segment has few partials, else behind it.
 
 // From the scores: the warps of a CTA that share tokens take every
@@ -1273,8 +1277,8 @@ __global__ void __launch_bounds__(128) cache_mass_kernel(const CacheAttnArgs a) 
 // Rows of a CTA of the join: with up to 8 rows or many partials a segment one, whose
 // partials go to D / 4 threads each, as many at once as fit; else as many rows as fit,
 // each going over its partials in turn (64 rows of 14 partials, with the weights beside
-// the join: 30.7 us against 34.0 one by one; 16 rows of 56: 38.8 against 30.5, of 222:
-// 86 against 64).
+// the join: 34.9 us against 36.7 one by one; 16 rows of 56: 41.4 against 32.8, 64 of 222:
+// 92 against 70).
 constexpr int kJoinFew = 16;
 __host__ __device__ __forceinline__ int join_rows(int seg_rows, int d, unsigned partials) {
   return seg_rows <= 8 || partials > kJoinFew ? 1 : 128 / (d / 4);

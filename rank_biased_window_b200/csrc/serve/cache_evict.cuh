@@ -16,7 +16,8 @@
 //
 // The move is bound by HBM, the selection by latency (a few thousand keys a CTA, four
 // digits, a meeting of the cluster for each): 64 heads of up to 16384 tokens, d = 128, cut
-// to 8192 take 55.5 us, of which the selection 13 (under ncu); 8 heads of 1000 tokens 9 us.
+// to 8192 take 55.7 us, of which the selection 13 (under ncu), and in place, where clusters
+// of up to 8 CTAs meet each round, 61.5; 8 heads of 1000 tokens 9 us, in place 12.
 #pragma once
 #include "../sm100.cuh"
 #include "e4m3.cuh"

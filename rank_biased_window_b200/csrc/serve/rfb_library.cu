@@ -90,7 +90,7 @@ size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 CaPlan plan_cache_attn(int B, int Hk, int R, int cap, int d, int r, bool mass, int sms) {
   CaPlan p;
-  // Up to 8 rows in a tile of 16 would be half empty: 44.5 us for 34.1 (4 rows, d = 128).
+  // Up to 8 rows in a tile of 16 would be half empty: 51.2 us for 35.2 (4 rows, d = 128).
   p.tile = R <= 8 ? 8 : 16;
   const int tiles = (R + p.tile - 1) / p.tile;
   p.wr = tiles >= 3 ? 4 : tiles;
@@ -112,11 +112,12 @@ CaPlan plan_cache_attn(int B, int Hk, int R, int cap, int d, int r, bool mass, i
   // A CTA a segment, which needs no join of partials and lets the hardware even out the
   // CTAs: for short contexts and for segments that fill several waves.  Measured over
   // 0.02 to 8 waves of segments (1 to 450 sequences of 8 heads, d = 64): up to four blocks a
-  // group of warps always (16 sequences to 128 tokens 5.7 us for 10.4, one of 500 tokens 7.0 for
-  // 8.2, of 1000 10.4 for 8.5), else up to 16 for each wave of segments (450 sequences to 4096
-  // tokens 194 us for 244, 225 to 1024 39 for 53, but 28 to 2048 20.2 for 15.7).  The same with
-  // the mass, whose second kernel runs in any case (112 sequences to 512 tokens 19.3 us for
-  // 24.5, one of 500 10.4 for 9.9), so that O and LSE do not depend on it.
+  // group of warps always (16 sequences to 128 tokens 6.2 us for 13.0, one of 500 tokens 7.5 for
+  // 11.6, of 1000 11.0 for 9.3), else up to 16 for each wave of segments (450 sequences to 4096
+  // tokens 207 us for 260, 225 to 1024 42 for 56, but 28 to 2048 21.9 for 17.3).  The same with
+  // the mass, whose second kernel runs in any case (112 sequences to 512 tokens 20.3 us for
+  // 25.8, one of 500 10.7 for 9.8), so that O and LSE do not depend on it.  By the capacity: the
+  // lengths are on the device, so a short context in a large cache is cut all the same.
   const long long segs = static_cast<long long>(B) * Hk * p.row_segs;
   const long long group = (cap / kCacheBlock + wts - 1) / wts;
   p.whole = group <= 4 || group * wave <= 16 * segs;

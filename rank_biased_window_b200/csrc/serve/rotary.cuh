@@ -10,7 +10,7 @@
 // what that leaves (up to 2^-26 of a turn, more than fp32's rounding of a sine near 0);
 // that work is done once per token and pair and used for every head of q and k the
 // thread goes over.  One read and one write of q and k: bound by HBM (2 x 16384 tokens,
-// 8 + 8 heads, d = 64, forward and backward: 47.5 us, 5.7 TB/s; 4097 tokens of 16 fp32
+// 8 + 8 heads, d = 64, forward and backward: 47.6 us, 5.6 TB/s; 4097 tokens of 16 fp32
 // heads, d = 128: 10.6 us, 6.3 TB/s).
 #pragma once
 #include <cstdint>
